@@ -218,6 +218,106 @@ DG_EXPORT int dg_m_grouped_fp8_gemm_nt_nopad(const void *a, const float *sfa, co
 DG_EXPORT int dg_fp8_gemm_nt_noalloc(const void *a, const float *sfa, const void *b, const float *sfb, void *d,
                                      int M, int N, int K, dg_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * Around the grouped GEMMs: dispatch, combine, SwiGLU and norms (the pages have no counterpart: they make the operands
+ * of the calls above and take their results).
+ *
+ * Common to them
+ *   - Activations are bf16 or fp32 (dg_dtype), row-major without gaps, 16-byte aligned, their width a multiple of 8.
+ *   - An output that a GEMM takes as its A is e4m3 with scales when its `..._sf` argument is given, else it has the
+ *     activations' type and `..._sf` is NULL.  The e4m3 output is laid out as the GEMMs take it: codes [rows][cols]
+ *     (cols % 128 == 0) and scales fp32, MN-major [groups][cols/128][dg_get_tma_aligned_size(rows_per_group, 4)],
+ *     16-byte aligned: rows_per_group is M_max in the masked layout and all rows otherwise.  A block's scale is
+ *     2^ceil(log2(amax / 448)) (1 for a block of zeros, at least 2^-126), the codes are round-to-nearest-even of
+ *     value / scale.  An infinite or NaN value becomes e4m3's NaN code, and its block's scale goes by the others.
+ *   - Sums, means and products are fp32 and rounded once.  Nothing depends on the order in which CTAs run: the same
+ *     inputs give the same bits.
+ *   - Rows that no slot or group owns are left as they were.
+ *   - Outputs must not overlap inputs or each other, except where a call says so.
+ *   - Each call is asynchronous on `stream` and takes no memory, but for the gradients of the norms (stream-ordered
+ *     scratch for the parameters' sums).  An empty call (no tokens or rows) launches nothing.
+ */
+typedef enum { DG_BF16 = 0, DG_F32 = 1 } dg_dtype;
+
+/* Rows that the contiguous layout can need at most for num_slots routed slots and G groups, under the alignment in
+ * force: every group that can have a row is padded.  DG_ERR_INVALID_ARG for num_slots < 0 or G < 1. */
+DG_EXPORT long long dg_moe_m_total_bound(long long num_slots, int G);
+
+/* Rows of the routed slots.  topk_ids [T][k]: the expert of each slot, int32 (id_bytes 4) or int64 (8), in [0, G), or -1
+ * for a slot that takes no row (an expert of another GPU, a padding token).  row_of_slot int32 [T][k]: the row of each
+ * slot, -1 if it has none.  Rows of a group are in the order of their slots (token by token).  1 <= k <= 32,
+ * 1 <= G <= 1024, T * k <= 2^30.  Another id is recorded as DG_ERR_BAD_GROUP (dg_check_device_error) and its slot gets no
+ * row.
+ *   contiguous: groups start at multiples of dg_get_m_alignment_for_contiguous_layout(); m_indices int32 [M_total] (16-byte
+ *     aligned) is written in full as the GEMM takes it, counts [G] as the rows of each group.  Slots that M_total has no
+ *     room for (see dg_moe_m_total_bound) get no row: DG_ERR_BAD_GROUP.
+ *   nopad: groups follow each other without gaps; counts [G].  Rows run to T * k at most.
+ *   masked: row g * M_max + i; masked_m [G].  Slots past M_max of their group get no row: DG_ERR_BAD_GROUP. */
+DG_EXPORT int dg_moe_sort_contiguous(const void *topk_ids, int id_bytes, int T, int k, int G, int M_total,
+                                     int *row_of_slot, int *m_indices, int *counts, dg_stream_t stream);
+DG_EXPORT int dg_moe_sort_nopad(const void *topk_ids, int id_bytes, int T, int k, int G, int *row_of_slot, int *counts,
+                                dg_stream_t stream);
+DG_EXPORT int dg_moe_sort_masked(const void *topk_ids, int id_bytes, int T, int k, int G, int M_max, int *row_of_slot,
+                                 int *masked_m, dg_stream_t stream);
+
+/* Dispatch: out[row_of_slot[t][s]] = x[t] for every slot with a row.  x [T][H] of `type`; out [rows][H] (masked:
+ * rows = G * M_max) of the same type, or e4m3 with out_sf.  row_of_slot names a row at most once; a row outside
+ * [-1, rows) is skipped and recorded as DG_ERR_BAD_GROUP.  Its gradient is dg_moe_unpermute without weights. */
+DG_EXPORT int dg_moe_permute(const void *x, int type, const int *row_of_slot, int T, int k, int H, int rows,
+                             int rows_per_group, void *out, float *out_sf, dg_stream_t stream);
+
+/* Combine: out[t] = sum over the slots s with a row of weights[t][s] * rows_in[row_of_slot[t][s]], in the slots' order
+ * (0 if there is none).  weights fp32 [T][k], NULL for 1.  rows_in [rows][H] and out [T][H] of `type`. */
+DG_EXPORT int dg_moe_unpermute(const void *rows_in, int type, const int *row_of_slot, const float *weights, int T, int k,
+                               int H, int rows, void *out, dg_stream_t stream);
+
+/* Gradient of the combine: d_rows[row_of_slot[t][s]] = weights[t][s] * d_out[t] (of `type`, or e4m3 with d_rows_sf) and
+ * d_weights[t][s] = <d_out[t], rows_in[row_of_slot[t][s]]> (0 for a slot without a row). */
+DG_EXPORT int dg_moe_unpermute_backward(const void *d_out, const void *rows_in, int type, const int *row_of_slot,
+                                        const float *weights, int T, int k, int H, int rows, int rows_per_group,
+                                        void *d_rows, float *d_rows_sf, float *d_weights, dg_stream_t stream);
+
+/* SwiGLU on the rows that the groups own: out = g * sigmoid(g) * u with gate_up [R][2 I] = [g | u].  Rows: one of
+ * m_indices [R] (contiguous), counts [G] (no padding) and masked_m [G] (masked, R = G * M_max), as the GEMM that wrote
+ * gate_up took it; all NULL: every row.  G is read with counts and masked_m.  out [R][I] of `type`, or e4m3 with out_sf.
+ * The gradient writes d_gate_up [R][2 I] = [d_g | d_u] from d_out [R][I]. */
+DG_EXPORT int dg_swiglu(const void *gate_up, int type, int R, int I, const int *m_indices, const int *counts,
+                        const int *masked_m, int G, void *out, float *out_sf, dg_stream_t stream);
+DG_EXPORT int dg_swiglu_backward(const void *d_out, const void *gate_up, int type, int R, int I, const int *m_indices,
+                                 const int *counts, const int *masked_m, int G, void *d_gate_up, float *d_gate_up_sf,
+                                 dg_stream_t stream);
+
+/* RMS norm before a block: out = x * r * weight, r = 1 / sqrt(mean(x^2) + eps) in every row of x [T][H] (H <= 16384).
+ * out has out_type, or is e4m3 with out_sf (out_type is then not looked at beyond its validity).  rstd fp32 [T] (may be
+ * NULL) keeps r for the gradient.  weight [H] of param_type.  Types: x and out bf16, or x fp32 and out bf16 or fp32.
+ * Gradient: d_x = d_skip + r * (weight d_out - x r^2 mean(weight d_out x)) of x's type, d_weight fp32 [H]; d_skip (x's
+ * type; NULL for 0; may be d_x) is the gradient that reaches x past the norm. */
+DG_EXPORT int dg_rms_norm(const void *x, int x_type, const void *weight, int param_type, float eps, int T, int H, void *out,
+                          int out_type, float *out_sf, float *rstd, dg_stream_t stream);
+DG_EXPORT int dg_rms_norm_backward(const void *d_out, const void *d_skip, const void *x, int x_type, int out_type,
+                                   const void *weight, int param_type, const float *rstd, int T, int H, void *d_x,
+                                   float *d_weight, dg_stream_t stream);
+
+/* The norms between two blocks, with the residual sum between them:
+ *     n = y * r_y * weight_post (n = y without weight_post),  x_out = x + alpha * gate * n,
+ *     out = x_out * r_x * weight (no out without weight),     r = 1 / sqrt(mean(square) + eps)
+ * x, x_out [T][H] of x_type (x_out may be x); y [T][H] and out of y_type (out e4m3 with out_sf); weight, weight_post [H] of
+ * param_type.  gate_kind 0: no gate; 1: gate [H] of param_type; 2: gate [T][H] of y_type.  rstd, rstd_post fp32 [T] (may
+ * be NULL) keep r_x and r_y.  out is made from x_out before its rounding.  Types as for dg_rms_norm.
+ * Gradient, from d_x_out (x_type; NULL for 0; may be d_x) and d_out (y_type), with x_out as stored: d_x (x_type), d_y
+ * (y_type), d_weight and d_weight_post fp32 [H], d_gate fp32 [H] (gate [H]) or y_type [T][H].  weight, d_out, x_out, rstd
+ * and d_weight go together, as do weight_post, rstd_post and d_weight_post, and gate and d_gate. */
+DG_EXPORT int dg_residual_rms_norm(const void *x, int x_type, const void *y, int y_type, const void *weight,
+                                   const void *weight_post, const void *gate, int gate_kind, int param_type, float alpha,
+                                   float eps, int T, int H, void *x_out, void *out, float *out_sf, float *rstd,
+                                   float *rstd_post, dg_stream_t stream);
+DG_EXPORT int dg_residual_rms_norm_backward(const void *d_x_out, const void *d_out, const void *x_out, int x_type,
+                                            const void *y, int y_type, const void *weight, const void *weight_post,
+                                            const void *gate, int gate_kind, int param_type, float alpha,
+                                            const float *rstd, const float *rstd_post, int T, int H, void *d_x,
+                                            void *d_y, float *d_weight, float *d_weight_post, void *d_gate,
+                                            dg_stream_t stream);
+
 /* Scale handling for the next calls on any thread ("promotion operations", DeepGEMM-for-PPU README,
  * "Optimizations"; the wrapper's disable_ue8m0_cast option).  0 (default): scales must be powers of two and are
  * applied by the block-scaled MMA (kind::mxf8f6f4, UE8M0 scales in tensor memory).  1: any finite fp32 scales;

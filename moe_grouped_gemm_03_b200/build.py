@@ -9,7 +9,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdg.so")
-SOURCES = [os.path.join(CSRC, "dg_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.cu", "moe_ops.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \
     [os.path.join(INCLUDE, "dg.h")]
 
@@ -41,7 +41,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc()] + flags(verbose) + SOURCES + ["-o", tmp]
+    # the sources are compiled side by side (they share no device code), then linked
+    cmd = [nvcc()] + flags(verbose) + ["--threads", str(len(SOURCES))] + SOURCES + ["-o", tmp]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     return LIB

@@ -1,0 +1,515 @@
+// Host side of the operators around the grouped GEMMs (include/dg.h): argument validation and launches of dispatch,
+// combine, SwiGLU and the norms on the caller's stream.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "dg.h"
+#include "dg_internal.h"
+#include "moe_rows.cuh"
+#include "moe_sort.cuh"
+#include "rms_norm.cuh"
+#include "swiglu.cuh"
+
+namespace {
+
+using dg::bf16;
+using dg::cuda_fail;
+using dg::fail;
+
+constexpr int kMaxRows = 1 << 30;  // rows and tokens of a call: row arithmetic stays within 32 bits
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool is_type(int t) { return t == DG_BF16 || t == DG_F32; }
+int aligned_rows(int rows) { return (rows + 3) / 4 * 4; }
+
+// Launches `kernel` as a programmatic dependent: it may be set up while the kernel before it on the stream ends, and
+// waits for that one (griddepcontrol.wait) before it touches memory.  Every kernel of this file does so at its start.
+template <typename... Params, typename... Args>
+int launch(const char *name, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int cluster, dg_stream_t stream,
+           Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? DG_OK : cuda_fail(e, name);
+}
+
+// ------------------------------------------------------------------------------------------------ dispatch: rows
+int check_sort(const void *topk_ids, int id_bytes, int T, int k, int G, const int *row_of_slot, const int *counts) {
+    if (!counts || (T > 0 && (!topk_ids || !row_of_slot))) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (id_bytes != 4 && id_bytes != 8) return fail(DG_ERR_INVALID_ARG, "id_bytes=%d must be 4 or 8", id_bytes);
+    if (topk_ids && topk_ids == row_of_slot) return fail(DG_ERR_INVALID_ARG, "row_of_slot must not be topk_ids");
+    if (!aligned(topk_ids, id_bytes) || !aligned(row_of_slot, 4) || !aligned(counts, 4))
+        return fail(DG_ERR_ALIGNMENT, "topk_ids, row_of_slot and counts must be aligned to their elements");
+    if (T < 0) return fail(DG_ERR_INVALID_ARG, "T=%d must be non-negative", T);
+    if (k < 1 || k > dg::MAX_TOPK) return fail(DG_ERR_INVALID_ARG, "k=%d must be in [1, %d]", k, dg::MAX_TOPK);
+    if (G < 1 || G > dg::SORT_MAX_GROUPS)
+        return fail(DG_ERR_INVALID_ARG, "G=%d must be in [1, %d]", G, dg::SORT_MAX_GROUPS);
+    if (static_cast<long long>(T) * k > kMaxRows) return fail(DG_ERR_INVALID_ARG, "T*k exceeds 2^30");
+    return DG_OK;
+}
+
+template <typename Id> int launch_sort(dg::SortParams p, int warps, int ctas, dg_stream_t stream) {
+    const size_t smem = sizeof(int) * dg::sort_smem_words(warps, p.G);
+    // above 48 KB the kernel has to be told so, once a device (each call that needs it says so: it is a host-side note)
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(dg::moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (sort)");
+    }
+    return launch("sort launch", dg::moe_sort_kernel<Id>, dim3(ctas), dim3(32 * warps), smem, ctas, stream, p);
+}
+
+int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) {
+    int device, sms;
+    if (int rc = dg::current_device(device, sms)) return rc;
+    p.slots = T * k;
+    p.err = dg::device_error_word();
+    if (!p.err) return fail(DG_ERR_CUDA, "device error word is not available");
+    int warps = (p.slots + 31) / 32;
+    const int ctas = warps > dg::SORT_MAX_WARPS ? 8 : 1;
+    warps = (warps + ctas - 1) / ctas;
+    warps = warps < 4 ? 4 : warps > dg::SORT_MAX_WARPS ? dg::SORT_MAX_WARPS : warps;
+    const int all = warps * ctas;
+    p.per_warp = ((p.slots + all - 1) / all + 31) / 32 * 32;
+    return id_bytes == 8 ? launch_sort<long long>(p, warps, ctas, stream) : launch_sort<int>(p, warps, ctas, stream);
+}
+
+// ----------------------------------------------------------------------------------------- dispatch and combine
+int check_rows(const void *x, const int *row_of_slot, const void *out, int type, int T, int k, int H, int rows) {
+    // (a tensor without elements may be null)
+    if (T > 0 && (!x || !row_of_slot || !out)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (!is_type(type)) return fail(DG_ERR_INVALID_ARG, "unknown element type %d", type);
+    if (T < 0 || T > kMaxRows || rows < 0 || rows > kMaxRows)
+        return fail(DG_ERR_INVALID_ARG, "T=%d and rows=%d must be in [0, 2^30]", T, rows);
+    if (k < 1 || k > dg::MAX_TOPK) return fail(DG_ERR_INVALID_ARG, "k=%d must be in [1, %d]", k, dg::MAX_TOPK);
+    if (H <= 0) return fail(DG_ERR_INVALID_ARG, "H=%d must be positive", H);
+    if (H % dg::VEC) return fail(DG_ERR_ALIGNMENT, "H=%d must be a multiple of %d", H, dg::VEC);
+    if (!aligned(x, 16) || !aligned(out, 16)) return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte aligned");
+    if (!aligned(row_of_slot, 4)) return fail(DG_ERR_ALIGNMENT, "row_of_slot must be 4-byte aligned");
+    return DG_OK;
+}
+
+// An e4m3 output's scales: rows in groups of rows_per_group, cols a multiple of 128.
+int scale_layout(dg::ScaleLayout &sf, float *out_sf, int rows, int rows_per_group, int cols) {
+    sf = dg::ScaleLayout{out_sf, 1, 4, 1};
+    if (!out_sf) return DG_OK;
+    if (cols % 128) return fail(DG_ERR_ALIGNMENT, "an e4m3 output's width %d must be a multiple of 128", cols);
+    if (!aligned(out_sf, 16)) return fail(DG_ERR_ALIGNMENT, "the scales must be 16-byte aligned");
+    if (rows > 0 && (rows_per_group < 1 || rows % rows_per_group))
+        return fail(DG_ERR_INVALID_ARG, "rows=%d must be a multiple of rows_per_group=%d", rows, rows_per_group);
+    if (rows > 0) sf = dg::ScaleLayout{out_sf, rows_per_group, aligned_rows(rows_per_group), cols / 128};
+    return DG_OK;
+}
+
+int rows_params(dg::RowsParams &p, const void *x, const int *row_of_slot, int T, int k, int H, int rows, void *out) {
+    int device, sms;
+    if (int rc = dg::current_device(device, sms)) return rc;
+    p.x = x;
+    p.row_of_slot = row_of_slot;
+    p.T = T;
+    p.k = k;
+    p.H = H;
+    p.rows = rows;
+    p.out = out;
+    p.err = dg::device_error_word();
+    return p.err ? DG_OK : fail(DG_ERR_CUDA, "device error word is not available");
+}
+
+unsigned row_ctas(long long items) { return static_cast<unsigned>((items + dg::ROWS_WARPS - 1) / dg::ROWS_WARPS); }
+int check_items(long long items) {
+    return items <= 0x7fffffffLL * dg::ROWS_WARPS ? DG_OK : fail(DG_ERR_INVALID_ARG, "T*H is out of range");
+}
+
+template <typename T, bool FP8> int launch_permute(dg::RowsParams p, dg_stream_t stream) {
+    constexpr int kSteps = 4;
+    p.segments = (p.H + kSteps * dg::STEP - 1) / (kSteps * dg::STEP);
+    if (int rc = check_items(p.T * p.segments)) return rc;
+    return launch("permute launch", dg::permute_kernel<T, FP8, kSteps>, dim3(row_ctas(p.T * p.segments)),
+                  dim3(32 * dg::ROWS_WARPS), 0, 1, stream, p);
+}
+
+template <typename T, bool FP8> int launch_unpermute_backward(const dg::RowsParams &p, dg_stream_t stream) {
+    const int steps = (p.H + dg::STEP - 1) / dg::STEP;
+    const int iters = (steps + 7) / 8;
+    const int warps = (steps + iters - 1) / iters;
+    return launch("combine gradient launch", dg::unpermute_backward_kernel<T, FP8>, dim3(static_cast<unsigned>(p.T)),
+                  dim3(32 * warps), 0, 1, stream, p);
+}
+
+// -------------------------------------------------------------------------------------------------------- SwiGLU
+template <typename T, bool FP8, bool BACKWARD> int launch_swiglu(dg::SwigluParams p, int sms, dg_stream_t stream) {
+    constexpr int kRows = BACKWARD ? 2 : 4;
+    const int ctas = (p.R + kRows * dg::SWIGLU_WARPS - 1) / (kRows * dg::SWIGLU_WARPS);
+    const int steps = (p.I + dg::STEP - 1) / dg::STEP;
+    int splits = (8 * sms + ctas - 1) / ctas;  // columns are split until the SMs are full
+    splits = splits > steps ? steps : splits;
+    const int per = (steps + splits - 1) / splits;
+    p.segment = per * dg::STEP;
+    return launch("swiglu launch", dg::swiglu_kernel<T, FP8, BACKWARD, kRows>, dim3(ctas, (steps + per - 1) / per),
+                  dim3(32 * dg::SWIGLU_WARPS), 0, 1, stream, p);
+}
+
+int swiglu_call(dg::SwigluParams p, int type, bool backward, const int *m_indices, const int *counts, const int *masked_m,
+                float *out_sf, dg_stream_t stream) {
+    if (p.R != 0 && (!p.gate_up || !p.out || (backward && !p.d_out))) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (!is_type(type)) return fail(DG_ERR_INVALID_ARG, "unknown element type %d", type);
+    if (p.R < 0 || p.R > kMaxRows) return fail(DG_ERR_INVALID_ARG, "R=%d must be in [0, 2^30]", p.R);
+    if (p.I <= 0 || p.I > (1 << 24)) return fail(DG_ERR_INVALID_ARG, "I=%d must be in [1, 2^24]", p.I);
+    if (p.I % dg::VEC) return fail(DG_ERR_ALIGNMENT, "I=%d must be a multiple of %d", p.I, dg::VEC);
+    if (out_sf && p.I % 128) return fail(DG_ERR_ALIGNMENT, "I=%d must be a multiple of 128 for an e4m3 output", p.I);
+    if (!aligned(p.gate_up, 16) || !aligned(p.out, 16) || !aligned(p.d_out, 16))
+        return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte aligned");
+    if ((m_indices != nullptr) + (counts != nullptr) + (masked_m != nullptr) > 1)
+        return fail(DG_ERR_INVALID_ARG, "at most one of m_indices, counts and masked_m may be given");
+    p.own = m_indices ? m_indices : counts ? counts : masked_m;
+    p.own_kind = m_indices ? dg::OWN_M_INDICES : counts ? dg::OWN_COUNTS : masked_m ? dg::OWN_MASKED : dg::OWN_ALL;
+    if (!aligned(p.own, 4)) return fail(DG_ERR_ALIGNMENT, "m_indices, counts and masked_m must be 4-byte aligned");
+    if ((counts || masked_m) && (p.G < 1 || p.G > dg::SORT_MAX_GROUPS))
+        return fail(DG_ERR_INVALID_ARG, "G=%d must be in [1, %d]", p.G, dg::SORT_MAX_GROUPS);
+    if (masked_m && p.R % p.G) return fail(DG_ERR_INVALID_ARG, "R=%d must be a multiple of G=%d", p.R, p.G);
+    p.rows_per_group = masked_m && p.R > 0 ? p.R / p.G : p.R;
+    if (int rc = scale_layout(p.sf, out_sf, p.R, p.rows_per_group, (backward ? 2 : 1) * p.I)) return rc;
+    if (p.R == 0) return DG_OK;
+    int device, sms;
+    if (int rc = dg::current_device(device, sms)) return rc;
+    if (type == DG_BF16) {
+        if (backward) return out_sf ? launch_swiglu<bf16, true, true>(p, sms, stream) : launch_swiglu<bf16, false, true>(p, sms, stream);
+        return out_sf ? launch_swiglu<bf16, true, false>(p, sms, stream) : launch_swiglu<bf16, false, false>(p, sms, stream);
+    }
+    if (backward) return out_sf ? launch_swiglu<float, true, true>(p, sms, stream) : launch_swiglu<float, false, true>(p, sms, stream);
+    return out_sf ? launch_swiglu<float, true, false>(p, sms, stream) : launch_swiglu<float, false, false>(p, sms, stream);
+}
+
+// --------------------------------------------------------------------------------------------------------- norms
+int check_norm(const dg::NormParams &p, int x_type, int y_type, int param_type) {
+    if (!is_type(x_type) || !is_type(y_type) || !is_type(param_type))
+        return fail(DG_ERR_INVALID_ARG, "unknown element type (%d, %d, %d)", x_type, y_type, param_type);
+    if (x_type == DG_BF16 && y_type == DG_F32)
+        return fail(DG_ERR_UNSUPPORTED, "a bf16 residual stream takes bf16 block outputs and norms only");
+    if (p.T < 0 || p.T > kMaxRows) return fail(DG_ERR_INVALID_ARG, "T=%d must be in [0, 2^30]", p.T);
+    if (p.H <= 0) return fail(DG_ERR_INVALID_ARG, "H=%d must be positive", p.H);
+    if (p.H > dg::NORM_MAX_H) return fail(DG_ERR_UNSUPPORTED, "H=%d exceeds %d", p.H, dg::NORM_MAX_H);
+    if (p.H % dg::VEC) return fail(DG_ERR_ALIGNMENT, "H=%d must be a multiple of %d", p.H, dg::VEC);
+    if (p.T != 0 && (p.gate_kind < dg::GATE_NONE || p.gate_kind > dg::GATE_TOKEN))
+        return fail(DG_ERR_INVALID_ARG, "gate_kind must be 0 without a gate, 1 ([H]) or 2 ([T][H]) with one");
+    for (const void *q : {p.x, p.y, p.w, p.w_post, p.gate, static_cast<const void *>(p.x_out),
+                          static_cast<const void *>(p.h), p.d_x_out, p.d_h, static_cast<const void *>(p.d_x),
+                          static_cast<const void *>(p.d_y), static_cast<const void *>(p.d_gate_token)})
+        if (!aligned(q, 16)) return fail(DG_ERR_ALIGNMENT, "tensors of the norms must be 16-byte aligned");
+    if (!aligned(p.rstd, 4) || !aligned(p.rstd_post, 4))
+        return fail(DG_ERR_ALIGNMENT, "rstd and rstd_post must be 4-byte aligned");
+    return DG_OK;
+}
+
+// -1 where the kind and the pointer do not go together (refused by check_norm).
+int gate_of(const void *gate, int kind) {
+    if (!gate) return kind == dg::GATE_NONE ? dg::GATE_NONE : -1;
+    return kind == dg::GATE_ROW || kind == dg::GATE_TOKEN ? kind : -1;
+}
+
+// Threads of a CTA and vectors of a thread for a row of H elements.
+void row_shape(int H, int &threads, int &iters) {
+    const int vecs = H / dg::VEC;
+    iters = vecs <= dg::NORM_MAX_THREADS ? 1 : vecs <= 2 * dg::NORM_MAX_THREADS ? 2 : 4;
+    threads = ((vecs + iters - 1) / iters + 31) / 32 * 32;
+}
+
+template <typename X, typename Y> int launch_norm(const dg::NormParams &p, dg_stream_t stream) {
+    int threads, iters;
+    row_shape(p.H, threads, iters);
+    auto kernel = iters == 1 ? dg::rms_norm_kernel<X, Y, 1>
+                             : iters == 2 ? dg::rms_norm_kernel<X, Y, 2> : dg::rms_norm_kernel<X, Y, 4>;
+    return launch("norm launch", kernel, dim3(static_cast<unsigned>(p.T)), dim3(threads), 0, 1, stream, p);
+}
+
+int norm_call(const dg::NormParams &p, int x_type, int y_type, int param_type, dg_stream_t stream) {
+    if (int rc = check_norm(p, x_type, y_type, param_type)) return rc;
+    if (p.T == 0) return DG_OK;
+    int device, sms;
+    if (int rc = dg::current_device(device, sms)) return rc;
+    if (x_type == DG_BF16) return launch_norm<bf16, bf16>(p, stream);
+    return y_type == DG_BF16 ? launch_norm<float, bf16>(p, stream) : launch_norm<float, float>(p, stream);
+}
+
+template <typename X, typename Y> int launch_norm_backward(const dg::NormParams &p, int ctas, dg_stream_t stream) {
+    int threads, iters;
+    row_shape(p.H, threads, iters);
+    auto kernel = iters == 1 ? dg::rms_norm_backward_kernel<X, Y, 1>
+                             : iters == 2 ? dg::rms_norm_backward_kernel<X, Y, 2> : dg::rms_norm_backward_kernel<X, Y, 4>;
+    return launch("norm gradient launch", kernel, dim3(ctas), dim3(threads), 0, 1, stream, p);
+}
+
+int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type, float *d_w, float *d_w_post,
+                       float *d_gate_row, dg_stream_t stream) {
+    if (int rc = check_norm(p, x_type, y_type, param_type)) return rc;
+    for (const float *q : {d_w, d_w_post, d_gate_row})
+        if (!aligned(q, 4)) return fail(DG_ERR_ALIGNMENT, "parameter gradients must be 4-byte aligned");
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (p.T == 0) {  // sums over no rows
+        for (float *q : {d_w, d_w_post, d_gate_row})
+            if (q && (e = cudaMemsetAsync(q, 0, sizeof(float) * p.H, s)) != cudaSuccess)
+                return cuda_fail(e, "cudaMemsetAsync (parameter gradients)");
+        return DG_OK;
+    }
+    int device, sms;
+    if (int rc = dg::current_device(device, sms)) return rc;
+    const int ctas = p.T < 2 * sms ? p.T : 2 * sms;
+    cudaMemPool_t pool;
+    if (int rc = dg::scratch_pool(device, pool)) return rc;
+    void *partial = nullptr;
+    e = cudaMallocFromPoolAsync(&partial, sizeof(float) * 3 * p.H * static_cast<size_t>(ctas), pool, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync (parameter gradients)");
+    p.partial = static_cast<float *>(partial);
+    int rc = x_type == DG_BF16   ? launch_norm_backward<bf16, bf16>(p, ctas, stream)
+             : y_type == DG_BF16 ? launch_norm_backward<float, bf16>(p, ctas, stream)
+                                 : launch_norm_backward<float, float>(p, ctas, stream);
+    if (rc == DG_OK && (d_w || d_w_post || d_gate_row))
+        rc = launch("norm gradient sum launch", dg::rms_norm_sum_kernel,
+                    dim3((p.H + dg::NORM_SUM_COLS - 1) / dg::NORM_SUM_COLS, 3), dim3(dg::NORM_SUM_COLS, dg::NORM_SUM_PARTS), 0,
+                    1, stream, static_cast<const float *>(p.partial), ctas, p.H, d_w, d_w_post, d_gate_row);
+    e = cudaFreeAsync(partial, s);
+    if (rc == DG_OK && e != cudaSuccess) rc = cuda_fail(e, "cudaFreeAsync (parameter gradients)");
+    return rc;
+}
+
+}  // namespace
+
+extern "C" {
+
+long long dg_moe_m_total_bound(long long num_slots, int G) {
+    if (num_slots < 0 || G < 1) return fail(DG_ERR_INVALID_ARG, "num_slots=%lld and G=%d are out of range", num_slots, G);
+    const long long a = dg::contiguous_alignment();
+    return (num_slots + (num_slots < G ? num_slots : G) * (a - 1)) / a * a;
+}
+
+int dg_moe_sort_contiguous(const void *topk_ids, int id_bytes, int T, int k, int G, int M_total, int *row_of_slot,
+                           int *m_indices, int *counts, dg_stream_t stream) {
+    if (int rc = check_sort(topk_ids, id_bytes, T, k, G, row_of_slot, counts)) return rc;
+    if (!m_indices && M_total > 0) return fail(DG_ERR_INVALID_ARG, "m_indices is null");
+    if (!aligned(m_indices, 16)) return fail(DG_ERR_ALIGNMENT, "m_indices must be 16-byte aligned");
+    const int a = dg::contiguous_alignment();
+    if (M_total < 0 || M_total > kMaxRows) return fail(DG_ERR_INVALID_ARG, "M_total=%d must be in [0, 2^30]", M_total);
+    if (M_total % a) return fail(DG_ERR_ALIGNMENT, "M_total=%d must be a multiple of %d", M_total, a);
+    dg::SortParams p{};
+    p.ids = topk_ids;
+    p.G = G;
+    p.layout = dg::SORT_CONTIGUOUS;
+    p.align = a;
+    p.M_total = M_total;
+    p.row_of_slot = row_of_slot;
+    p.m_indices = m_indices;
+    p.counts = counts;
+    return sort_call(p, id_bytes, T, k, stream);
+}
+
+int dg_moe_sort_nopad(const void *topk_ids, int id_bytes, int T, int k, int G, int *row_of_slot, int *counts,
+                      dg_stream_t stream) {
+    if (int rc = check_sort(topk_ids, id_bytes, T, k, G, row_of_slot, counts)) return rc;
+    dg::SortParams p{};
+    p.ids = topk_ids;
+    p.G = G;
+    p.layout = dg::SORT_NOPAD;
+    p.row_of_slot = row_of_slot;
+    p.counts = counts;
+    return sort_call(p, id_bytes, T, k, stream);
+}
+
+int dg_moe_sort_masked(const void *topk_ids, int id_bytes, int T, int k, int G, int M_max, int *row_of_slot, int *masked_m,
+                       dg_stream_t stream) {
+    if (int rc = check_sort(topk_ids, id_bytes, T, k, G, row_of_slot, masked_m)) return rc;
+    if (M_max < 1 || static_cast<long long>(G) * M_max > kMaxRows)
+        return fail(DG_ERR_INVALID_ARG, "M_max=%d must be positive and G*M_max at most 2^30", M_max);
+    dg::SortParams p{};
+    p.ids = topk_ids;
+    p.G = G;
+    p.layout = dg::SORT_MASKED;
+    p.M_max = M_max;
+    p.row_of_slot = row_of_slot;
+    p.counts = masked_m;
+    return sort_call(p, id_bytes, T, k, stream);
+}
+
+int dg_moe_permute(const void *x, int type, const int *row_of_slot, int T, int k, int H, int rows, int rows_per_group,
+                   void *out, float *out_sf, dg_stream_t stream) {
+    dg::RowsParams p{};
+    if (rows == 0) T = 0;  // nowhere to write
+    if (int rc = check_rows(x, row_of_slot, out, type, T, k, H, rows)) return rc;
+    if (int rc = scale_layout(p.sf, out_sf, rows, rows_per_group, H)) return rc;
+    if (T == 0) return DG_OK;
+    if (int rc = rows_params(p, x, row_of_slot, T, k, H, rows, out)) return rc;
+    if (type == DG_BF16) return out_sf ? launch_permute<bf16, true>(p, stream) : launch_permute<bf16, false>(p, stream);
+    return out_sf ? launch_permute<float, true>(p, stream) : launch_permute<float, false>(p, stream);
+}
+
+int dg_moe_unpermute(const void *rows_in, int type, const int *row_of_slot, const float *weights, int T, int k, int H,
+                     int rows, void *out, dg_stream_t stream) {
+    dg::RowsParams p{};
+    if (rows == 0) rows_in = out;  // (no row is read)
+    if (int rc = check_rows(rows_in, row_of_slot, out, type, T, k, H, rows)) return rc;
+    if (!aligned(weights, 4)) return fail(DG_ERR_ALIGNMENT, "weights must be 4-byte aligned");
+    if (T == 0) return DG_OK;
+    if (int rc = rows_params(p, rows_in, row_of_slot, T, k, H, rows, out)) return rc;
+    p.weights = weights;
+    p.segments = (H + dg::STEP - 1) / dg::STEP;
+    if (int rc = check_items(p.T * p.segments)) return rc;
+    const dim3 grid(row_ctas(p.T * p.segments)), block(32 * dg::ROWS_WARPS);
+    if (type == DG_BF16) return launch("combine launch", dg::unpermute_kernel<bf16, 8>, grid, block, 0, 1, stream, p);
+    return launch("combine launch", dg::unpermute_kernel<float, 4>, grid, block, 0, 1, stream, p);
+}
+
+int dg_moe_unpermute_backward(const void *d_out, const void *rows_in, int type, const int *row_of_slot,
+                              const float *weights, int T, int k, int H, int rows, int rows_per_group, void *d_rows,
+                              float *d_rows_sf, float *d_weights, dg_stream_t stream) {
+    dg::RowsParams p{};
+    if (rows == 0) rows_in = d_rows = const_cast<void *>(d_out);  // (no row is read or written)
+    if (int rc = check_rows(rows_in, row_of_slot, d_rows, type, T, k, H, rows)) return rc;
+    if (T > 0 && (!d_out || !weights || !d_weights)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(d_out, 16)) return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte aligned");
+    if (!aligned(weights, 4) || !aligned(d_weights, 4))
+        return fail(DG_ERR_ALIGNMENT, "weights and d_weights must be 4-byte aligned");
+    if (int rc = scale_layout(p.sf, d_rows_sf, rows, rows_per_group, H)) return rc;
+    if (T == 0) return DG_OK;
+    if (int rc = rows_params(p, rows_in, row_of_slot, T, k, H, rows, d_rows)) return rc;
+    p.d_out = d_out;
+    p.weights = weights;
+    p.d_weights = d_weights;
+    if (type == DG_BF16)
+        return d_rows_sf ? launch_unpermute_backward<bf16, true>(p, stream) : launch_unpermute_backward<bf16, false>(p, stream);
+    return d_rows_sf ? launch_unpermute_backward<float, true>(p, stream) : launch_unpermute_backward<float, false>(p, stream);
+}
+
+int dg_swiglu(const void *gate_up, int type, int R, int I, const int *m_indices, const int *counts, const int *masked_m,
+              int G, void *out, float *out_sf, dg_stream_t stream) {
+    dg::SwigluParams p{};
+    p.gate_up = gate_up;
+    p.out = out;
+    p.G = G;
+    p.R = R;
+    p.I = I;
+    return swiglu_call(p, type, false, m_indices, counts, masked_m, out_sf, stream);
+}
+
+int dg_swiglu_backward(const void *d_out, const void *gate_up, int type, int R, int I, const int *m_indices,
+                       const int *counts, const int *masked_m, int G, void *d_gate_up, float *d_gate_up_sf,
+                       dg_stream_t stream) {
+    dg::SwigluParams p{};
+    p.gate_up = gate_up;
+    p.d_out = d_out;
+    p.out = d_gate_up;
+    p.G = G;
+    p.R = R;
+    p.I = I;
+    return swiglu_call(p, type, true, m_indices, counts, masked_m, d_gate_up_sf, stream);
+}
+
+int dg_residual_rms_norm(const void *x, int x_type, const void *y, int y_type, const void *weight, const void *weight_post,
+                         const void *gate, int gate_kind, int param_type, float alpha, float eps, int T, int H, void *x_out,
+                         void *out, float *out_sf, float *rstd, float *rstd_post, dg_stream_t stream) {
+    dg::NormParams p{};
+    if (T != 0 && (!x || !y || !x_out)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (T != 0 && (weight != nullptr) != (out != nullptr)) return fail(DG_ERR_INVALID_ARG, "weight and out go together");
+    if (T != 0 && out_sf && !out) return fail(DG_ERR_INVALID_ARG, "scales without an output");
+    if (rstd && !weight) return fail(DG_ERR_INVALID_ARG, "rstd without weight");
+    if (rstd_post && !weight_post) return fail(DG_ERR_INVALID_ARG, "rstd_post without weight_post");
+    if (int rc = scale_layout(p.sf, out_sf, T, T, H)) return rc;
+    p.x = x;
+    p.y = y;
+    p.w = weight;
+    p.w_post = weight_post;
+    p.gate = gate;
+    p.gate_kind = gate_of(gate, gate_kind);
+    p.x_out = x_out;
+    p.h = out;
+    p.rstd = rstd;
+    p.rstd_post = rstd_post;
+    p.alpha = alpha;
+    p.eps = eps;
+    p.T = T;
+    p.H = H;
+    p.param_f32 = param_type == DG_F32;
+    return norm_call(p, x_type, y_type, param_type, stream);
+}
+
+int dg_rms_norm(const void *x, int x_type, const void *weight, int param_type, float eps, int T, int H, void *out,
+                int out_type, float *out_sf, float *rstd, dg_stream_t stream) {
+    dg::NormParams p{};
+    if (!weight || (T != 0 && (!x || !out))) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (int rc = scale_layout(p.sf, out_sf, T, T, H)) return rc;
+    p.x = x;
+    p.w = weight;
+    p.h = out;
+    p.rstd = rstd;
+    p.eps = eps;
+    p.T = T;
+    p.H = H;
+    p.param_f32 = param_type == DG_F32;
+    return norm_call(p, x_type, out_type, param_type, stream);
+}
+
+int dg_residual_rms_norm_backward(const void *d_x_out, const void *d_out, const void *x_out, int x_type, const void *y,
+                                  int y_type, const void *weight, const void *weight_post, const void *gate, int gate_kind,
+                                  int param_type, float alpha, const float *rstd, const float *rstd_post, int T, int H,
+                                  void *d_x, void *d_y, float *d_weight, float *d_weight_post, void *d_gate,
+                                  dg_stream_t stream) {
+    dg::NormParams p{};
+    if (T != 0 && (!y || !d_x || !d_y)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    if (weight && (!d_weight || (T != 0 && (!d_out || !x_out || !rstd))))
+        return fail(DG_ERR_INVALID_ARG, "weight needs d_out, x_out, rstd and d_weight");
+    if (!weight && (d_out || d_weight)) return fail(DG_ERR_INVALID_ARG, "d_out and d_weight need weight");
+    if (weight_post && (!d_weight_post || (T != 0 && !rstd_post)))
+        return fail(DG_ERR_INVALID_ARG, "weight_post needs rstd_post and d_weight_post");
+    if (!weight_post && d_weight_post) return fail(DG_ERR_INVALID_ARG, "d_weight_post needs weight_post");
+    if (T != 0 && (gate != nullptr) != (d_gate != nullptr)) return fail(DG_ERR_INVALID_ARG, "gate and d_gate go together");
+    if (T != 0 && !d_x_out && !weight) return fail(DG_ERR_INVALID_ARG, "no gradient comes in: give d_x_out or weight and d_out");
+    p.x = x_out;
+    p.y = y;
+    p.w = weight;
+    p.w_post = weight_post;
+    p.gate = gate;
+    p.gate_kind = gate_of(gate, gate_kind);
+    p.rstd = const_cast<float *>(rstd);
+    p.rstd_post = const_cast<float *>(rstd_post);
+    p.d_x_out = d_x_out;
+    p.d_h = d_out;
+    p.d_x = d_x;
+    p.d_y = d_y;
+    p.d_gate_token = p.gate_kind == dg::GATE_TOKEN ? d_gate : nullptr;
+    p.alpha = alpha;
+    p.T = T;
+    p.H = H;
+    p.param_f32 = param_type == DG_F32;
+    return norm_backward_call(p, x_type, y_type, param_type, d_weight, d_weight_post,
+                              p.gate_kind == dg::GATE_ROW ? static_cast<float *>(d_gate) : nullptr, stream);
+}
+
+int dg_rms_norm_backward(const void *d_out, const void *d_skip, const void *x, int x_type, int out_type, const void *weight,
+                         int param_type, const float *rstd, int T, int H, void *d_x, float *d_weight, dg_stream_t stream) {
+    dg::NormParams p{};
+    if (!weight || !d_weight || (T != 0 && (!d_out || !x || !rstd || !d_x))) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
+    p.x = x;
+    p.w = weight;
+    p.rstd = const_cast<float *>(rstd);
+    p.d_x_out = d_skip;
+    p.d_h = d_out;
+    p.d_x = d_x;
+    p.T = T;
+    p.H = H;
+    p.param_f32 = param_type == DG_F32;
+    return norm_backward_call(p, x_type, out_type, param_type, d_weight, nullptr, nullptr, stream);
+}
+
+}  // extern "C"

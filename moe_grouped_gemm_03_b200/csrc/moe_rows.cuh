@@ -1,0 +1,206 @@
+// Rows to the experts and back: dispatch (gather of the tokens into the operand of a grouped GEMM, quantised on the
+// way), combine (weighted sum of a token's expert rows) and the combine's gradient.  All three go by tokens and read
+// row_of_slot [T][k]; a slot without a row (-1) takes no part.
+//
+//   permute            a[row(t, s)] = x[t]                       (e4m3: codes and scales of the token, made once)
+//   unpermute          out[t] = sum_s w(t, s) * rows[row(t, s)]
+//   its gradient       d_rows[row(t, s)] = w(t, s) * d_out[t],  d_w(t, s) = <d_out[t], rows[row(t, s)]>
+//
+// All are bound by HBM: every byte of a token's row is read once, whatever k is.
+#pragma once
+#include "rowwise.cuh"
+
+namespace dg {
+
+constexpr int MAX_TOPK = 32;     // one lane of a warp for each slot of a token
+constexpr int ROWS_WARPS = 8;    // warps of a CTA (permute, unpermute)
+constexpr int STEP = 32 * VEC;   // elements of one step of a warp
+
+struct RowsParams {
+    const void *x;           // permute: x [T][H]; unpermute and gradient: rows [rows][H]
+    const void *d_out;       // gradient: [T][H]
+    const int *row_of_slot;  // [T][k]
+    const float *weights;    // [T][k]; null: 1 (unpermute)
+    void *out;               // permute, gradient: [rows][H]; unpermute: [T][H]
+    float *d_weights;        // gradient: [T][k]
+    ScaleLayout sf;
+    long long T;
+    int k, H, rows, segments;  // segments: parts of a row, each a warp's work
+    unsigned *err;
+};
+
+// Lane s's row of slot s of the token: -1 if there is none (or it is out of range, which is recorded).
+__device__ __forceinline__ int slot_row(const RowsParams &p, long long token, int s) {
+    if (s >= p.k) return -1;
+    const int row = __ldg(p.row_of_slot + token * p.k + s);
+    if (row >= p.rows || row < -1) raise_bad_group(p.err);
+    return row < p.rows ? row : -1;
+}
+
+template <typename T, bool FP8, int STEPS>
+__global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long item = static_cast<long long>(blockIdx.x) * ROWS_WARPS + (threadIdx.x >> 5);
+    const long long token = item / p.segments;
+    if (token >= p.T) return;
+    const int row = slot_row(p, token, lane);
+    const unsigned live = __ballot_sync(0xffffffffu, row >= 0);
+    if (!live) return;
+    const int begin = static_cast<int>(item - token * p.segments) * STEPS * STEP + lane * VEC;
+    const T *x = static_cast<const T *>(p.x) + token * p.H;
+    Raw8<T> r[STEPS];
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j)
+        if (begin + j * STEP < p.H) r[j].load(x + begin + j * STEP);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+        const int col = begin + j * STEP;
+        const bool in = col < p.H;
+        if constexpr (FP8) {
+            float v[VEC] = {}, scale;
+            if (in) r[j].get(v);
+            const uint2 q = quantise8(v, block_amax(v), scale);
+            for (unsigned m = live; m; m &= m - 1) {
+                const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
+                if (in) *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + at * p.H + col) = q;
+            }
+            // lanes s and 16 + s of the warp write slot s's scales of its two blocks
+            for (int s = 0; s < p.k; s += BLOCK_LANES) {
+                const int at = __shfl_sync(0xffffffffu, row, s + (lane & 15));
+                if (in && at >= 0) *p.sf.at(at, col >> 7) = scale;
+            }
+        } else {
+            for (unsigned m = live; m; m &= m - 1) {
+                const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
+                if (in) r[j].store(static_cast<T *>(p.out) + at * p.H + col);
+            }
+        }
+    }
+}
+
+// The sum is taken in fp32 in the slots' order and rounded once; U rows' loads are in flight at a time.
+template <typename T, int U>
+__global__ void __launch_bounds__(32 * ROWS_WARPS) unpermute_kernel(const RowsParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long item = static_cast<long long>(blockIdx.x) * ROWS_WARPS + (threadIdx.x >> 5);
+    const long long token = item / p.segments;
+    if (token >= p.T) return;
+    const int row = slot_row(p, token, lane);
+    const float w = row >= 0 && p.weights ? __ldg(p.weights + token * p.k + lane) : 1.f;
+    const int col = static_cast<int>(item - token * p.segments) * STEP + lane * VEC;
+    const bool in = col < p.H;
+    const T *rows = static_cast<const T *>(p.x) + (in ? col : 0);
+    float acc[VEC] = {};
+    unsigned m = __ballot_sync(0xffffffffu, row >= 0);
+    while (m) {
+        Raw8<T> r[U];
+        float weight[U];
+        int n = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m) {
+                const int s = __ffs(m) - 1;
+                m &= m - 1;
+                const long long at = __shfl_sync(0xffffffffu, row, s);
+                weight[u] = __shfl_sync(0xffffffffu, w, s);
+                r[u].load(rows + at * p.H);
+                n = u + 1;
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < n) {
+                float v[VEC];
+                r[u].get(v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] = fmaf(weight[u], v[i], acc[i]);
+            }
+    }
+    if (in) store8(static_cast<T *>(p.out) + token * p.H + col, acc);
+}
+
+constexpr int GRAD_SLOTS = 8;       // slots of a token at a time
+constexpr int GRAD_MAX_WARPS = 16;
+
+// One CTA a token: the inner products need whole rows.  fp32 sums, in an order that does not change.
+template <typename T, bool FP8>
+__global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel(const RowsParams p) {
+    __shared__ float part[GRAD_SLOTS][GRAD_MAX_WARPS];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const long long token = blockIdx.x;
+    const int row = slot_row(p, token, lane);
+    const float w = lane < p.k ? __ldg(p.weights + token * p.k + lane) : 0.f;
+    const T *d_out = static_cast<const T *>(p.d_out) + token * p.H;
+    const T *rows = static_cast<const T *>(p.x);
+    for (int first = 0; first < p.k; first += GRAD_SLOTS) {
+        int at[GRAD_SLOTS];
+        float weight[GRAD_SLOTS], acc[GRAD_SLOTS] = {};
+#pragma unroll
+        for (int u = 0; u < GRAD_SLOTS; ++u) {
+            at[u] = __shfl_sync(0xffffffffu, row, (first + u) & 31);
+            if (first + u >= p.k) at[u] = -1;
+            weight[u] = __shfl_sync(0xffffffffu, w, (first + u) & 31);
+        }
+        for (int base = warp * STEP; base < p.H; base += warps * STEP) {
+            const int col = base + lane * VEC;
+            const bool in = col < p.H;
+            Raw8<T> r[GRAD_SLOTS];
+#pragma unroll
+            for (int u = 0; u < GRAD_SLOTS; ++u)
+                if (at[u] >= 0 && in) r[u].load(rows + static_cast<long long>(at[u]) * p.H + col);
+            float d[VEC] = {}, amax = 0.f, keep = 0.f;
+            if (in) load8(d_out + col, d);
+            if constexpr (FP8) amax = block_amax(d);
+#pragma unroll
+            for (int u = 0; u < GRAD_SLOTS; ++u)
+                if (at[u] >= 0) {
+                    if (in) {
+                        float v[VEC];
+                        r[u].get(v);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) acc[u] = fmaf(d[i], v[i], acc[u]);
+                    }
+                    float g[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) g[i] = weight[u] * d[i];
+                    if constexpr (FP8) {
+                        // rounding keeps order: the largest of the rounded products is the product of the largest
+                        float scale;
+                        const uint2 q = quantise8(g, fabsf(weight[u]) * amax, scale);
+                        if ((lane & 15) == u) keep = scale;
+                        if (in)
+                            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) +
+                                                       static_cast<long long>(at[u]) * p.H + col) = q;
+                    } else if (in) {
+                        store8(static_cast<T *>(p.out) + static_cast<long long>(at[u]) * p.H + col, g);
+                    }
+                }
+            if constexpr (FP8) {
+                const int mine = __shfl_sync(0xffffffffu, row, (first + (lane & 15)) & 31);
+                if (in && (lane & 15) < GRAD_SLOTS && first + (lane & 15) < p.k && mine >= 0)
+                    *p.sf.at(mine, col >> 7) = keep;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < GRAD_SLOTS; ++u) {
+            float sum = acc[u];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) part[u][warp] = sum;
+        }
+        __syncthreads();
+        if (threadIdx.x < GRAD_SLOTS && first + threadIdx.x < p.k) {
+            float sum = 0.f;
+            for (int i = 0; i < warps; ++i) sum += part[threadIdx.x][i];
+            p.d_weights[token * p.k + first + threadIdx.x] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace dg
