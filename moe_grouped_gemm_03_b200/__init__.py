@@ -435,47 +435,71 @@ def m_grouped_fp8_gemm_nt_nopad(lhs, rhs, out: torch.Tensor, counts: torch.Tenso
 _ACT_TYPES = (torch.bfloat16, torch.float32)
 _TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}  # dg_dtype
 _ID_TYPES = (torch.int32, torch.int64)
+_F32, _I32 = (torch.float32,), (torch.int32,)
 
 
 def _check_tensors(*named) -> None:
-    """(name, tensor, shape, dtypes) of every argument of a row-wise call: contiguous CUDA tensors, all on the current
-    device (on whose current stream the call runs)."""
-    device = torch.cuda.current_device()
+    """(name, tensor, shape, dtypes) of the arguments of a row-wise call: contiguous CUDA tensors, all on the current
+    device, on whose current stream the call runs.  The passing path is a handful of attribute look-ups and formats no
+    message: these calls last a few microseconds."""
+    device = torch._C._cuda_getDevice()
     for name, t, shape, dtypes in named:
-        if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous() \
-                and t.is_cuda and t.get_device() == device:
-            continue
-        _need(isinstance(t, torch.Tensor), lambda: f"{name} must be a torch.Tensor")
-        _need(t.dtype in dtypes, lambda: f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-        _need(t.shape == shape, lambda: f"{name} must be {list(shape)}, got {list(t.shape)}")
-        _need(t.is_contiguous(), lambda: f"{name} must be contiguous")
-        _need(t.is_cuda, lambda: f"{name} must be a CUDA tensor")
-        _need(False, lambda: f"{name} is on device {t.get_device()}, the current one is {device}")
+        try:
+            if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+                continue
+        except AttributeError:
+            pass
+        _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
+        _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+        _need(t.shape == shape, f"{name} must be {list(shape)}, got {list(t.shape)}")
+        _need(t.is_contiguous(), f"{name} must be contiguous")
+        _need(t.is_cuda, f"{name} must be a CUDA tensor")
+        _need(False, f"{name} is on device {t.get_device()}, the current one is {device}")
 
 
-def _dims(name, t, *dims):
-    """Shape of a tensor argument that has one of the numbers of dimensions `dims`."""
-    _need(isinstance(t, torch.Tensor), lambda: f"{name} must be a torch.Tensor")
-    _need(t.dim() in dims, lambda: f"{name} must have {' or '.join(map(str, dims))} dims, got {tuple(t.shape)}")
-    return t.shape
+def _check_optional(*named) -> None:
+    """The same for arguments that may be None."""
+    _check_tensors(*[n for n in named if n[1] is not None])
+
+
+def _raw_stream() -> int:
+    """The current stream of the current device, without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _dims(name, t, least, most=None):
+    """Shape of a tensor argument that has `least` (or up to `most`) dimensions."""
+    try:
+        shape = t.shape
+        if least <= len(shape) <= (most or least):
+            return shape
+    except AttributeError:
+        pass
+    _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
+    raise DGError(-1, f"{name} must have {least if most is None else f'{least} or {most}'} dims, got {tuple(t.shape)}")
 
 
 def _row_operand(name, out, cols, dtype):
     """A row operand, [rows, cols] or [G, M_max, cols]: a tensor of `dtype`, or (e4m3 codes, sf) as a GEMM's lhs.
     Returns (codes or tensor, sf or None, rows, rows_per_group)."""
     if isinstance(out, (tuple, list)):
-        _need(len(out) == 2, lambda: f"{name} must be a tensor or a pair (codes, scales)")
+        if not (len(out) == 2):
+            raise DGError(-1, f"{name} must be a tensor or a pair (codes, scales)")
         a, sf = out
         shape = _dims(name, a, 2, 3)
+        if not (isinstance(sf, torch.Tensor)):
+            raise DGError(-1, f"{name} scales must be a torch.Tensor")
         per = shape[-2]
-        _check_tensors((name, a, (*shape[:-1], cols), _FP8_TYPES),
-                       (name + " scales", sf, (*shape[:-2], cols // 128, get_tma_aligned_size(per, 4)), (torch.float32,)))
+        groups = shape[:-2]
+        _check_tensors((name, a, (*groups, per, cols), _FP8_TYPES),
+                       (name + " scales", sf, (*groups, cols // 128, (per + 3) // 4 * 4), _F32))
     else:
         a, sf = out, None
         shape = _dims(name, a, 2, 3)
         per = shape[-2]
-        _check_tensors((name, a, (*shape[:-1], cols), (dtype,)))
-    return a, sf, per * (shape[0] if len(shape) == 3 else 1), per
+        groups = shape[:-2]
+        _check_tensors((name, a, (*groups, per, cols), (dtype,)))
+    return a, sf, per * groups[0] if groups else per, per
 
 
 def get_m_total_bound(num_slots: int, num_groups: int) -> int:
@@ -489,8 +513,8 @@ def get_m_total_bound(num_slots: int, num_groups: int) -> int:
 def _sort_args(topk_ids, row_of_slot, counts):
     T, k = _dims("topk_ids", topk_ids, 2)
     G, = _dims("counts", counts, 1)
-    _check_tensors(("topk_ids", topk_ids, (T, k), _ID_TYPES), ("row_of_slot", row_of_slot, (T, k), (torch.int32,)),
-                   ("counts", counts, (G,), (torch.int32,)))
+    _check_tensors(("topk_ids", topk_ids, (T, k), _ID_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32),
+                   ("counts", counts, (G,), _I32))
     return _ptr(topk_ids), topk_ids.element_size(), T, k, G
 
 
@@ -501,22 +525,22 @@ def moe_sort_contiguous(topk_ids: torch.Tensor, row_of_slot: torch.Tensor, m_ind
     get_m_total_bound, or any multiple of the alignment that has room), counts int32 [G] rows of each group."""
     args = _sort_args(topk_ids, row_of_slot, counts)
     M, = _dims("m_indices", m_indices, 1)
-    _check_tensors(("m_indices", m_indices, (M,), (torch.int32,)))
-    _check(_lib.dg_moe_sort_contiguous(*args, M, _ptr(row_of_slot), _ptr(m_indices), _ptr(counts), _stream()))
+    _check_tensors(("m_indices", m_indices, (M,), _I32))
+    _check(_lib.dg_moe_sort_contiguous(*args, M, _ptr(row_of_slot), _ptr(m_indices), _ptr(counts), _raw_stream()))
 
 
 def moe_sort_nopad(topk_ids: torch.Tensor, row_of_slot: torch.Tensor, counts: torch.Tensor) -> None:
     """Rows of the routed slots in the no-padding layout: row_of_slot int32 [T, k], counts int32 [G] as
     m_grouped_fp8_gemm_nt_nopad takes them."""
     args = _sort_args(topk_ids, row_of_slot, counts)
-    _check(_lib.dg_moe_sort_nopad(*args, _ptr(row_of_slot), _ptr(counts), _stream()))
+    _check(_lib.dg_moe_sort_nopad(*args, _ptr(row_of_slot), _ptr(counts), _raw_stream()))
 
 
 def moe_sort_masked(topk_ids: torch.Tensor, row_of_slot: torch.Tensor, masked_m: torch.Tensor, m_max: int) -> None:
     """Rows of the routed slots in the masked layout (row g * m_max + i): row_of_slot int32 [T, k], masked_m int32 [G] as
     m_grouped_fp8_gemm_nt_masked takes it.  Slots past m_max of their group get no row (DG_ERR_BAD_GROUP)."""
     args = _sort_args(topk_ids, row_of_slot, masked_m)
-    _check(_lib.dg_moe_sort_masked(*args, int(m_max), _ptr(row_of_slot), _ptr(masked_m), _stream()))
+    _check(_lib.dg_moe_sort_masked(*args, int(m_max), _ptr(row_of_slot), _ptr(masked_m), _raw_stream()))
 
 
 def moe_permute(x: torch.Tensor, row_of_slot: torch.Tensor, out) -> None:
@@ -525,10 +549,10 @@ def moe_permute(x: torch.Tensor, row_of_slot: torch.Tensor, out) -> None:
     moe_unpermute of the rows' gradient without weights."""
     T, H = _dims("x", x, 2)
     _, k = _dims("row_of_slot", row_of_slot, 2)
-    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), (torch.int32,)))
+    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32))
     a, sf, rows, per = _row_operand("out", out, H, x.dtype)
     _check(_lib.dg_moe_permute(_ptr(x), _TYPE_CODES[x.dtype], _ptr(row_of_slot), T, k, H, rows, per, _ptr(a), _ptr(sf),
-                               _stream()))
+                               _raw_stream()))
 
 
 def moe_unpermute(rows: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tensor,
@@ -538,12 +562,12 @@ def moe_unpermute(rows: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tens
     shape = _dims("rows", rows, 2, 3)
     H, R = shape[-1], shape[-2] * (shape[0] if len(shape) == 3 else 1)
     T, k = _dims("row_of_slot", row_of_slot, 2)
-    _check_tensors(("rows", rows, shape, _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), (torch.int32,)),
+    _check_tensors(("rows", rows, shape, _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32),
                    ("out", out, (T, H), (rows.dtype,)))
     if weights is not None:
-        _check_tensors(("weights", weights, (T, k), (torch.float32,)))
+        _check_tensors(("weights", weights, (T, k), _F32))
     _check(_lib.dg_moe_unpermute(_ptr(rows), _TYPE_CODES[rows.dtype], _ptr(row_of_slot), _ptr(weights), T, k, H, R,
-                                 _ptr(out), _stream()))
+                                 _ptr(out), _raw_stream()))
 
 
 def moe_unpermute_backward(d_out: torch.Tensor, rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor,
@@ -553,30 +577,32 @@ def moe_unpermute_backward(d_out: torch.Tensor, rows: torch.Tensor, row_of_slot:
     shape = _dims("rows", rows, 2, 3)
     H = shape[-1]
     T, k = _dims("row_of_slot", row_of_slot, 2)
-    _check_tensors(("rows", rows, shape, _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), (torch.int32,)),
-                   ("d_out", d_out, (T, H), (rows.dtype,)), ("weights", weights, (T, k), (torch.float32,)),
-                   ("d_weights", d_weights, (T, k), (torch.float32,)))
+    _check_tensors(("rows", rows, shape, _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32),
+                   ("d_out", d_out, (T, H), (rows.dtype,)), ("weights", weights, (T, k), _F32),
+                   ("d_weights", d_weights, (T, k), _F32))
     a, sf, R, per = _row_operand("d_rows", d_rows, H, rows.dtype)
-    _need(a.shape == shape, lambda: f"d_rows must be shaped as rows, {list(shape)}, got {list(a.shape)}")
+    if not (a.shape == shape):
+        raise DGError(-1, f"d_rows must be shaped as rows, {list(shape)}, got {list(a.shape)}")
     _check(_lib.dg_moe_unpermute_backward(_ptr(d_out), _ptr(rows), _TYPE_CODES[rows.dtype], _ptr(row_of_slot),
-                                          _ptr(weights), T, k, H, R, per, _ptr(a), _ptr(sf), _ptr(d_weights), _stream()))
+                                          _ptr(weights), T, k, H, R, per, _ptr(a), _ptr(sf), _ptr(d_weights), _raw_stream()))
 
 
 def _swiglu_args(gate_up, out, out_name, out_cols, m_indices, counts, masked_m):
     shape = gate_up.shape
     a, sf, R, per = _row_operand(out_name, out, out_cols, gate_up.dtype)
-    _need(a.shape[:-1] == shape[:-1], lambda: f"{out_name} must have the rows of gate_up, {list(shape[:-1])}")
+    if not (a.shape[:-1] == shape[:-1]):
+        raise DGError(-1, f"{out_name} must have the rows of gate_up, {list(shape[:-1])}")
     _need((m_indices is not None) + (counts is not None) + (masked_m is not None) <= 1,
           "at most one of m_indices, counts and masked_m may be given")
     G = 0
     if m_indices is not None:
-        _check_tensors(("m_indices", m_indices, (R,), (torch.int32,)))
+        _check_tensors(("m_indices", m_indices, (R,), _I32))
     elif counts is not None:
         G, = _dims("counts", counts, 1)
-        _check_tensors(("counts", counts, (G,), (torch.int32,)))
+        _check_tensors(("counts", counts, (G,), _I32))
     elif masked_m is not None:
         G, = _dims("masked_m", masked_m, 1)
-        _check_tensors(("masked_m", masked_m, (G,), (torch.int32,)))
+        _check_tensors(("masked_m", masked_m, (G,), _I32))
     _need((len(shape) == 3) == (masked_m is not None) and (masked_m is None or G == shape[0]),
           "tensors of three dims [G, M_max, ...] go with masked_m [G], and masked_m with them")
     return a, sf, R, G
@@ -593,7 +619,7 @@ def swiglu(gate_up: torch.Tensor, out, m_indices: Optional[torch.Tensor] = None,
     _check_tensors(("gate_up", gate_up, shape, _ACT_TYPES))
     a, sf, R, G = _swiglu_args(gate_up, out, "out", I, m_indices, counts, masked_m)
     _check(_lib.dg_swiglu(_ptr(gate_up), _TYPE_CODES[gate_up.dtype], R, I, _ptr(m_indices), _ptr(counts), _ptr(masked_m),
-                          G, _ptr(a), _ptr(sf), _stream()))
+                          G, _ptr(a), _ptr(sf), _raw_stream()))
 
 
 def swiglu_backward(d_out: torch.Tensor, gate_up: torch.Tensor, d_gate_up, m_indices: Optional[torch.Tensor] = None,
@@ -606,11 +632,7 @@ def swiglu_backward(d_out: torch.Tensor, gate_up: torch.Tensor, d_gate_up, m_ind
     _check_tensors(("gate_up", gate_up, shape, _ACT_TYPES), ("d_out", d_out, (*shape[:-1], I), (gate_up.dtype,)))
     a, sf, R, G = _swiglu_args(gate_up, d_gate_up, "d_gate_up", 2 * I, m_indices, counts, masked_m)
     _check(_lib.dg_swiglu_backward(_ptr(d_out), _ptr(gate_up), _TYPE_CODES[gate_up.dtype], R, I, _ptr(m_indices),
-                                   _ptr(counts), _ptr(masked_m), G, _ptr(a), _ptr(sf), _stream()))
-
-
-def _optional(*named) -> None:
-    _check_tensors(*(n for n in named if n[1] is not None))
+                                   _ptr(counts), _ptr(masked_m), G, _ptr(a), _ptr(sf), _raw_stream()))
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, out, eps: float = 1e-6, rstd: Optional[torch.Tensor] = None) -> None:
@@ -622,11 +644,13 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, out, eps: float = 1e-6, rstd
     out_type = torch.bfloat16 if pair else getattr(out, "dtype", None)
     _need(out_type in _ACT_TYPES, "out must be bf16 or fp32, or a pair (e4m3, sfa)")
     _check_tensors(("x", x, (T, H), _ACT_TYPES), ("weight", weight, (H,), _ACT_TYPES))
-    _optional(("rstd", rstd, (T,), (torch.float32,)))
+    if rstd is not None:
+        _check_tensors(("rstd", rstd, (T,), _F32))
     a, sf, R, _ = _row_operand("out", out, H, out_type)
-    _need(tuple(a.shape) == (T, H), lambda: f"out must be {[T, H]}, got {list(a.shape)}")
+    if not (tuple(a.shape) == (T, H)):
+        raise DGError(-1, f"out must be {[T, H]}, got {list(a.shape)}")
     _check(_lib.dg_rms_norm(_ptr(x), _TYPE_CODES[x.dtype], _ptr(weight), _TYPE_CODES[weight.dtype], eps, T, H, _ptr(a),
-                            _TYPE_CODES[out_type], _ptr(sf), _ptr(rstd), _stream()))
+                            _TYPE_CODES[out_type], _ptr(sf), _ptr(rstd), _raw_stream()))
 
 
 def rms_norm_backward(d_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, d_x: torch.Tensor,
@@ -634,26 +658,25 @@ def rms_norm_backward(d_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     """Gradient of rms_norm: d_x [T, H] of x's type, plus d_skip (the gradient that reaches x past the norm; may be d_x
     itself), and d_weight fp32 [H].  d_out [T, H] of the forward's output type before quantisation."""
     T, H = _dims("x", x, 2)
-    f32 = (torch.float32,)
-    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("weight", weight, (H,), _ACT_TYPES), ("rstd", rstd, (T,), f32),
+    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("weight", weight, (H,), _ACT_TYPES), ("rstd", rstd, (T,), _F32),
                    ("d_out", d_out, (T, H), _ACT_TYPES), ("d_x", d_x, (T, H), (x.dtype,)),
-                   ("d_weight", d_weight, (H,), f32))
-    _optional(("d_skip", d_skip, (T, H), (x.dtype,)))
+                   ("d_weight", d_weight, (H,), _F32))
+    if d_skip is not None:
+        _check_tensors(("d_skip", d_skip, (T, H), (x.dtype,)))
     _check(_lib.dg_rms_norm_backward(_ptr(d_out), _ptr(d_skip), _ptr(x), _TYPE_CODES[x.dtype], _TYPE_CODES[d_out.dtype],
                                      _ptr(weight), _TYPE_CODES[weight.dtype], _ptr(rstd), T, H, _ptr(d_x),
-                                     _ptr(d_weight), _stream()))
+                                     _ptr(d_weight), _raw_stream()))
 
 
 def _norm_params(H, T, y_dtype, weight, weight_post, gate):
     """(gate kind, type code of the parameters) of a residual norm: weight, weight_post and a gate [H] have one type."""
-    kind = 0 if gate is None else 1 if gate.dim() == 1 else 2
-    params = [(n, p) for n, p in (("weight", weight), ("weight_post", weight_post), ("gate", gate if kind == 1 else None))
-              if p is not None]
-    dtype = params[0][1].dtype if params else torch.float32
-    _need(dtype in _ACT_TYPES, lambda: f"{params[0][0]} has dtype {dtype}, expected one of {_ACT_TYPES}")
-    _check_tensors(*((n, p, (H,), (dtype,)) for n, p in params))
-    if kind == 2:
-        _check_tensors(("gate", gate, (T, H), (y_dtype,)))
+    kind = 0 if gate is None else 1 if len(_dims("gate", gate, 1, 2)) == 1 else 2
+    first = weight if weight is not None else weight_post if weight_post is not None else gate if kind == 1 else None
+    dtype = getattr(first, "dtype", torch.float32)
+    if not (dtype in _ACT_TYPES):
+        raise DGError(-1, f"the norms' parameters have dtype {dtype}, expected one of {_ACT_TYPES}")
+    _check_optional(("weight", weight, (H,), (dtype,)), ("weight_post", weight_post, (H,), (dtype,)),
+                    ("gate", gate, (H,) if kind == 1 else (T, H), (dtype,) if kind == 1 else (y_dtype,)))
     return kind, _TYPE_CODES[dtype]
 
 
@@ -667,16 +690,17 @@ def residual_rms_norm(x: torch.Tensor, y: torch.Tensor, x_out: torch.Tensor, wei
     fp32) or [T, H] (y's type).  rstd and rstd_post fp32 [T] keep r_x and r_y for residual_rms_norm_backward."""
     T, H = _dims("x", x, 2)
     _check_tensors(("x", x, (T, H), _ACT_TYPES), ("y", y, (T, H), _ACT_TYPES), ("x_out", x_out, (T, H), (x.dtype,)))
+    _check_optional(("rstd", rstd, (T,), _F32), ("rstd_post", rstd_post, (T,), _F32))
     kind, param_type = _norm_params(H, T, y.dtype, weight, weight_post, gate)
     _need((weight is None) == (out is None), "weight and out go together")
-    _optional(("rstd", rstd, (T,), (torch.float32,)), ("rstd_post", rstd_post, (T,), (torch.float32,)))
     a = sf = None
     if out is not None:
         a, sf, _, _ = _row_operand("out", out, H, y.dtype)
-        _need(tuple(a.shape) == (T, H), lambda: f"out must be {[T, H]}, got {list(a.shape)}")
+        if not (tuple(a.shape) == (T, H)):
+            raise DGError(-1, f"out must be {[T, H]}, got {list(a.shape)}")
     _check(_lib.dg_residual_rms_norm(_ptr(x), _TYPE_CODES[x.dtype], _ptr(y), _TYPE_CODES[y.dtype], _ptr(weight),
                                      _ptr(weight_post), _ptr(gate), kind, param_type, alpha, eps, T, H, _ptr(x_out),
-                                     _ptr(a), _ptr(sf), _ptr(rstd), _ptr(rstd_post), _stream()))
+                                     _ptr(a), _ptr(sf), _ptr(rstd), _ptr(rstd_post), _raw_stream()))
 
 
 def residual_rms_norm_backward(d_x_out: Optional[torch.Tensor], y: torch.Tensor, d_x: torch.Tensor, d_y: torch.Tensor,
@@ -690,17 +714,16 @@ def residual_rms_norm_backward(d_x_out: Optional[torch.Tensor], y: torch.Tensor,
     the forward stored it, y, the parameters, rstd and rstd_post.  Goes out: d_x (x's type; may be d_x_out), d_y (y's type),
     d_weight and d_weight_post fp32 [H], d_gate fp32 [H] for a gate [H], or of y's type for a gate [T, H]."""
     T, H = _dims("y", y, 2)
-    f32 = (torch.float32,)
     _check_tensors(("y", y, (T, H), _ACT_TYPES), ("d_y", d_y, (T, H), (y.dtype,)), ("d_x", d_x, (T, H), _ACT_TYPES))
     kind, param_type = _norm_params(H, T, y.dtype, weight, weight_post, gate)
-    _optional(("d_x_out", d_x_out, (T, H), (d_x.dtype,)), ("d_out", d_out, (T, H), (y.dtype,)),
-              ("x_out", x_out, (T, H), (d_x.dtype,)), ("rstd", rstd, (T,), f32), ("rstd_post", rstd_post, (T,), f32),
-              ("d_weight", d_weight, (H,), f32), ("d_weight_post", d_weight_post, (H,), f32),
-              ("d_gate", d_gate, (H,) if kind == 1 else (T, H), f32 if kind == 1 else (y.dtype,)))
+    _check_optional(("d_x_out", d_x_out, (T, H), (d_x.dtype,)), ("d_out", d_out, (T, H), (y.dtype,)),
+                    ("x_out", x_out, (T, H), (d_x.dtype,)), ("rstd", rstd, (T,), _F32), ("rstd_post", rstd_post, (T,), _F32),
+                    ("d_weight", d_weight, (H,), _F32), ("d_weight_post", d_weight_post, (H,), _F32),
+                    ("d_gate", d_gate, (H,) if kind == 1 else (T, H), _F32 if kind == 1 else (y.dtype,)))
     _check(_lib.dg_residual_rms_norm_backward(
         _ptr(d_x_out), _ptr(d_out), _ptr(x_out), _TYPE_CODES[d_x.dtype], _ptr(y), _TYPE_CODES[y.dtype], _ptr(weight),
         _ptr(weight_post), _ptr(gate), kind, param_type, alpha, _ptr(rstd), _ptr(rstd_post), T, H, _ptr(d_x), _ptr(d_y),
-        _ptr(d_weight), _ptr(d_weight_post), _ptr(d_gate), _stream()))
+        _ptr(d_weight), _ptr(d_weight_post), _ptr(d_gate), _raw_stream()))
 
 
 __all__ = [

@@ -21,6 +21,8 @@ using dg::fail;
 constexpr int kMaxRows = 1 << 30;  // rows and tokens of a call: row arithmetic stays within 32 bits
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Vectors of eight elements: 16 bytes of bf16, 32 of fp32.
+bool vec_aligned(const void *p, int type) { return aligned(p, type == DG_F32 ? 32 : 16); }
 bool is_type(int t) { return t == DG_BF16 || t == DG_F32; }
 int aligned_rows(int rows) { return (rows + 3) / 4 * 4; }
 
@@ -61,15 +63,18 @@ int check_sort(const void *topk_ids, int id_bytes, int T, int k, int G, const in
     return DG_OK;
 }
 
-template <typename Id> int launch_sort(dg::SortParams p, int warps, int ctas, dg_stream_t stream) {
-    const size_t smem = sizeof(int) * dg::sort_smem_words(warps, p.G);
-    // above 48 KB the kernel has to be told so, once a device (each call that needs it says so: it is a host-side note)
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(dg::moe_sort_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (sort)");
-    }
-    return launch("sort launch", dg::moe_sort_kernel<Id>, dim3(ctas), dim3(32 * warps), smem, ctas, stream, p);
+template <typename Id, bool ONE> int launch_sort(const dg::SortParams &p, int warps, int ctas, dg_stream_t stream) {
+    const size_t smem = sizeof(int) * dg::sort_smem_words(p.slot_warps, p.G);
+    // notes on the kernel, made anew by each call that needs them: more than 48 KB, a cluster of more than 8
+    cudaError_t e;
+    if (smem > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(dg::moe_sort_kernel<Id, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(smem))) != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute (sort)");
+    if (ctas > 8 && (e = cudaFuncSetAttribute(dg::moe_sort_kernel<Id, ONE>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                              1)) != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute (sort cluster)");
+    return launch("sort launch", dg::moe_sort_kernel<Id, ONE>, dim3(ctas), dim3(32 * warps), smem, ctas, stream, p);
 }
 
 int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) {
@@ -79,16 +84,26 @@ int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) 
     p.err = dg::device_error_word();
     if (!p.err) return fail(DG_ERR_CUDA, "device error word is not available");
     int warps = (p.slots + 31) / 32;
-    const int ctas = warps > dg::SORT_MAX_WARPS ? 8 : 1;
+    // Measured (us, 256 groups, one CTA / 8 / 16): 256 slots 2.9 / 3.8 / -, 1024 slots 6.2 / 3.8 / -, 2048 slots
+    // 7.0 / 3.9 / 3.9, 8192 slots - / 5.3 / 4.3, 65536 slots - / 10.4 / 7.9.
+    const int ctas = warps > 32 ? 16 : warps > 8 ? 8 : 1;
     warps = (warps + ctas - 1) / ctas;
-    warps = warps < 4 ? 4 : warps > dg::SORT_MAX_WARPS ? dg::SORT_MAX_WARPS : warps;
-    const int all = warps * ctas;
+    p.slot_warps = warps < 1 ? 1 : warps > dg::SORT_MAX_WARPS ? dg::SORT_MAX_WARPS : warps;
+    const int all = p.slot_warps * ctas;
     p.per_warp = ((p.slots + all - 1) / all + 31) / 32 * 32;
-    return id_bytes == 8 ? launch_sort<long long>(p, warps, ctas, stream) : launch_sort<int>(p, warps, ctas, stream);
+    while ((1 << p.id_bits) < p.G) ++p.id_bits;
+    // a thread for each group's column too
+    const int group_warps = (p.G + 31) / 32;
+    warps = p.slot_warps > group_warps ? p.slot_warps : group_warps;
+    const bool one = p.per_warp <= 32 * dg::SORT_BATCHES;
+    if (id_bytes == 8)
+        return one ? launch_sort<long long, true>(p, warps, ctas, stream) : launch_sort<long long, false>(p, warps, ctas, stream);
+    return one ? launch_sort<int, true>(p, warps, ctas, stream) : launch_sort<int, false>(p, warps, ctas, stream);
 }
 
 // ----------------------------------------------------------------------------------------- dispatch and combine
-int check_rows(const void *x, const int *row_of_slot, const void *out, int type, int T, int k, int H, int rows) {
+// (out_type: DG_BF16 for e4m3 codes too, whose alignment is the same)
+int check_rows(const void *x, const int *row_of_slot, const void *out, int type, int out_type, int T, int k, int H, int rows) {
     // (a tensor without elements may be null)
     if (T > 0 && (!x || !row_of_slot || !out)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
     if (!is_type(type)) return fail(DG_ERR_INVALID_ARG, "unknown element type %d", type);
@@ -97,7 +112,8 @@ int check_rows(const void *x, const int *row_of_slot, const void *out, int type,
     if (k < 1 || k > dg::MAX_TOPK) return fail(DG_ERR_INVALID_ARG, "k=%d must be in [1, %d]", k, dg::MAX_TOPK);
     if (H <= 0) return fail(DG_ERR_INVALID_ARG, "H=%d must be positive", H);
     if (H % dg::VEC) return fail(DG_ERR_ALIGNMENT, "H=%d must be a multiple of %d", H, dg::VEC);
-    if (!aligned(x, 16) || !aligned(out, 16)) return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte aligned");
+    if (!vec_aligned(x, type) || !vec_aligned(out, out_type))
+        return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");
     if (!aligned(row_of_slot, 4)) return fail(DG_ERR_ALIGNMENT, "row_of_slot must be 4-byte aligned");
     return DG_OK;
 }
@@ -170,8 +186,8 @@ int swiglu_call(dg::SwigluParams p, int type, bool backward, const int *m_indice
     if (p.I <= 0 || p.I > (1 << 24)) return fail(DG_ERR_INVALID_ARG, "I=%d must be in [1, 2^24]", p.I);
     if (p.I % dg::VEC) return fail(DG_ERR_ALIGNMENT, "I=%d must be a multiple of %d", p.I, dg::VEC);
     if (out_sf && p.I % 128) return fail(DG_ERR_ALIGNMENT, "I=%d must be a multiple of 128 for an e4m3 output", p.I);
-    if (!aligned(p.gate_up, 16) || !aligned(p.out, 16) || !aligned(p.d_out, 16))
-        return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte aligned");
+    if (!vec_aligned(p.gate_up, type) || !vec_aligned(p.out, out_sf ? DG_BF16 : type) || !vec_aligned(p.d_out, type))
+        return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");
     if ((m_indices != nullptr) + (counts != nullptr) + (masked_m != nullptr) > 1)
         return fail(DG_ERR_INVALID_ARG, "at most one of m_indices, counts and masked_m may be given");
     p.own = m_indices ? m_indices : counts ? counts : masked_m;
@@ -205,10 +221,13 @@ int check_norm(const dg::NormParams &p, int x_type, int y_type, int param_type) 
     if (p.H % dg::VEC) return fail(DG_ERR_ALIGNMENT, "H=%d must be a multiple of %d", p.H, dg::VEC);
     if (p.T != 0 && (p.gate_kind < dg::GATE_NONE || p.gate_kind > dg::GATE_TOKEN))
         return fail(DG_ERR_INVALID_ARG, "gate_kind must be 0 without a gate, 1 ([H]) or 2 ([T][H]) with one");
-    for (const void *q : {p.x, p.y, p.w, p.w_post, p.gate, static_cast<const void *>(p.x_out),
-                          static_cast<const void *>(p.h), p.d_x_out, p.d_h, static_cast<const void *>(p.d_x),
-                          static_cast<const void *>(p.d_y), static_cast<const void *>(p.d_gate_token)})
-        if (!aligned(q, 16)) return fail(DG_ERR_ALIGNMENT, "tensors of the norms must be 16-byte aligned");
+    const int gate_type = p.gate_kind == dg::GATE_ROW ? param_type : y_type;
+    if (!vec_aligned(p.x, x_type) || !vec_aligned(p.x_out, x_type) || !vec_aligned(p.d_x_out, x_type) ||
+        !vec_aligned(p.d_x, x_type) || !vec_aligned(p.y, y_type) || !vec_aligned(p.d_h, y_type) ||
+        !vec_aligned(p.d_y, y_type) || !vec_aligned(p.d_gate_token, y_type) ||
+        !vec_aligned(p.h, p.sf.sf ? static_cast<int>(DG_BF16) : y_type) || !vec_aligned(p.w, param_type) ||
+        !vec_aligned(p.w_post, param_type) || !vec_aligned(p.gate, gate_type))
+        return fail(DG_ERR_ALIGNMENT, "tensors of the norms must be 16-byte (fp32: 32-byte) aligned");
     if (!aligned(p.rstd, 4) || !aligned(p.rstd_post, 4))
         return fail(DG_ERR_ALIGNMENT, "rstd and rstd_post must be 4-byte aligned");
     return DG_OK;
@@ -347,7 +366,7 @@ int dg_moe_permute(const void *x, int type, const int *row_of_slot, int T, int k
                    void *out, float *out_sf, dg_stream_t stream) {
     dg::RowsParams p{};
     if (rows == 0) T = 0;  // nowhere to write
-    if (int rc = check_rows(x, row_of_slot, out, type, T, k, H, rows)) return rc;
+    if (int rc = check_rows(x, row_of_slot, out, type, out_sf ? DG_BF16 : type, T, k, H, rows)) return rc;
     if (int rc = scale_layout(p.sf, out_sf, rows, rows_per_group, H)) return rc;
     if (T == 0) return DG_OK;
     if (int rc = rows_params(p, x, row_of_slot, T, k, H, rows, out)) return rc;
@@ -359,7 +378,7 @@ int dg_moe_unpermute(const void *rows_in, int type, const int *row_of_slot, cons
                      int rows, void *out, dg_stream_t stream) {
     dg::RowsParams p{};
     if (rows == 0) rows_in = out;  // (no row is read)
-    if (int rc = check_rows(rows_in, row_of_slot, out, type, T, k, H, rows)) return rc;
+    if (int rc = check_rows(rows_in, row_of_slot, out, type, type, T, k, H, rows)) return rc;
     if (!aligned(weights, 4)) return fail(DG_ERR_ALIGNMENT, "weights must be 4-byte aligned");
     if (T == 0) return DG_OK;
     if (int rc = rows_params(p, rows_in, row_of_slot, T, k, H, rows, out)) return rc;
@@ -376,9 +395,9 @@ int dg_moe_unpermute_backward(const void *d_out, const void *rows_in, int type, 
                               float *d_rows_sf, float *d_weights, dg_stream_t stream) {
     dg::RowsParams p{};
     if (rows == 0) rows_in = d_rows = const_cast<void *>(d_out);  // (no row is read or written)
-    if (int rc = check_rows(rows_in, row_of_slot, d_rows, type, T, k, H, rows)) return rc;
+    if (int rc = check_rows(rows_in, row_of_slot, d_rows, type, d_rows_sf ? DG_BF16 : type, T, k, H, rows)) return rc;
     if (T > 0 && (!d_out || !weights || !d_weights)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
-    if (!aligned(d_out, 16)) return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte aligned");
+    if (!vec_aligned(d_out, type)) return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");
     if (!aligned(weights, 4) || !aligned(d_weights, 4))
         return fail(DG_ERR_ALIGNMENT, "weights and d_weights must be 4-byte aligned");
     if (int rc = scale_layout(p.sf, d_rows_sf, rows, rows_per_group, H)) return rc;

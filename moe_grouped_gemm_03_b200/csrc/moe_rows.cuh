@@ -32,11 +32,13 @@ struct RowsParams {
 // Lane s's row of slot s of the token: -1 if there is none (or it is out of range, which is recorded).
 __device__ __forceinline__ int slot_row(const RowsParams &p, long long token, int s) {
     if (s >= p.k) return -1;
-    const int row = __ldg(p.row_of_slot + token * p.k + s);
+    const int row = *(p.row_of_slot + token * p.k + s);
     if (row >= p.rows || row < -1) raise_bad_group(p.err);
     return row < p.rows ? row : -1;
 }
 
+// A warp takes STEPS * 256 columns of a token: all loads first, then each block is quantised once, then the slots in turn,
+// so that a slot's address is made once for all of its stores.
 template <typename T, bool FP8, int STEPS>
 __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsParams p) {
     grid_dependency_wait();
@@ -54,28 +56,38 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsPara
 #pragma unroll
     for (int j = 0; j < STEPS; ++j)
         if (begin + j * STEP < p.H) r[j].load(x + begin + j * STEP);
+    if constexpr (FP8) {
+        uint2 q[STEPS];
+        float scale[STEPS];
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-        const int col = begin + j * STEP;
-        const bool in = col < p.H;
-        if constexpr (FP8) {
-            float v[VEC] = {}, scale;
-            if (in) r[j].get(v);
-            const uint2 q = quantise8(v, block_amax(v), scale);
-            for (unsigned m = live; m; m &= m - 1) {
-                const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
-                if (in) *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + at * p.H + col) = q;
-            }
-            // lanes s and 16 + s of the warp write slot s's scales of its two blocks
-            for (int s = 0; s < p.k; s += BLOCK_LANES) {
-                const int at = __shfl_sync(0xffffffffu, row, s + (lane & 15));
-                if (in && at >= 0) *p.sf.at(at, col >> 7) = scale;
-            }
-        } else {
-            for (unsigned m = live; m; m &= m - 1) {
-                const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
-                if (in) r[j].store(static_cast<T *>(p.out) + at * p.H + col);
-            }
+        for (int j = 0; j < STEPS; ++j) {
+            float v[VEC] = {};
+            if (begin + j * STEP < p.H) r[j].get(v);
+            q[j] = quantise8(v, block_amax(v), scale[j]);
+        }
+        for (unsigned m = live; m; m &= m - 1) {
+            const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
+            uint8_t *out = static_cast<uint8_t *>(p.out) + at * p.H + begin;
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j)
+                if (begin + j * STEP < p.H) *reinterpret_cast<uint2 *>(out + j * STEP) = q[j];
+        }
+        // lanes s and 16 + s of the warp write slot s's scales of a step's two blocks
+        for (int s = 0; s < p.k; s += BLOCK_LANES) {
+            const int at = __shfl_sync(0xffffffffu, row, s + (lane & 15));
+            if (at < 0) continue;
+            float *sf = p.sf.at(at, begin >> 7);
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j)
+                if (begin + j * STEP < p.H) sf[static_cast<long long>(j) * (STEP / 128) * p.sf.ld] = scale[j];
+        }
+    } else {
+        for (unsigned m = live; m; m &= m - 1) {
+            const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
+            T *out = static_cast<T *>(p.out) + at * p.H + begin;
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j)
+                if (begin + j * STEP < p.H) r[j].store(out + j * STEP);
         }
     }
 }
@@ -90,7 +102,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) unpermute_kernel(const RowsPa
     const long long token = item / p.segments;
     if (token >= p.T) return;
     const int row = slot_row(p, token, lane);
-    const float w = row >= 0 && p.weights ? __ldg(p.weights + token * p.k + lane) : 1.f;
+    const float w = row >= 0 && p.weights ? *(p.weights + token * p.k + lane) : 1.f;
     const int col = static_cast<int>(item - token * p.segments) * STEP + lane * VEC;
     const bool in = col < p.H;
     const T *rows = static_cast<const T *>(p.x) + (in ? col : 0);
@@ -134,7 +146,7 @@ __global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const long long token = blockIdx.x;
     const int row = slot_row(p, token, lane);
-    const float w = lane < p.k ? __ldg(p.weights + token * p.k + lane) : 0.f;
+    const float w = lane < p.k ? *(p.weights + token * p.k + lane) : 0.f;
     const T *d_out = static_cast<const T *>(p.d_out) + token * p.H;
     const T *rows = static_cast<const T *>(p.x);
     for (int first = 0; first < p.k; first += GRAD_SLOTS) {

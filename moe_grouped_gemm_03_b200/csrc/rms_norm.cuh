@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
             if (p.d_x_out && col < p.H) load8(static_cast<const X *>(p.d_x_out) + at + col, dx[j]);
         }
         if (p.w) {
-            const float r = __ldg(p.rstd + row);
+            const float r = *(p.rstd + row);
             float x[ITERS][VEC], e[ITERS][VEC], sum = 0.f;
 #pragma unroll
             for (int j = 0; j < ITERS; ++j) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
             __syncthreads();  // part[0] is written again in the next row
             continue;
         }
-        const float r = p.w_post ? __ldg(p.rstd_post + row) : 1.f;
+        const float r = p.w_post ? *(p.rstd_post + row) : 1.f;
         float y[ITERS][VEC], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < ITERS; ++j) {

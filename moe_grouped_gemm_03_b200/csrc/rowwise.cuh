@@ -27,11 +27,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// One lane's vector of eight elements as it lies in memory (bf16: 16 bytes, fp32: 32 bytes).
+// Loads are ordinary ones, not the non-coherent kind (__ldg): a kernel here may start before the one that writes its
+// inputs has ended, and memory that changes during a kernel's life is not for that path.
+
+// One lane's vector of eight elements as it lies in memory (bf16: 16 bytes, fp32: 32 bytes, each at a multiple of that).
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16> {
     uint4 a;
-    __device__ __forceinline__ void load(const bf16 *p) { a = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load(const bf16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
         unpack_bf16x2(a.x, v[0], v[1]);
@@ -44,22 +47,25 @@ template <> struct Raw8<bf16> {
                        pack_bf16x2(v[6], v[7]));
     }
 };
-template <> struct Raw8<float> {
-    float4 a, b;
+template <> struct Raw8<float> {  // one 256-bit access: as two of 128 bits, half of each request's sectors went unused
+    float v8[VEC];
     __device__ __forceinline__ void load(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v8[0]), "=f"(v8[1]), "=f"(v8[2]), "=f"(v8[3]), "=f"(v8[4]), "=f"(v8[5]), "=f"(v8[6]), "=f"(v8[7])
+                     : "l"(p));
     }
     __device__ __forceinline__ void store(float *p) const {
-        reinterpret_cast<float4 *>(p)[0] = a;
-        reinterpret_cast<float4 *>(p)[1] = b;
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v8[0]), "f"(v8[1]), "f"(v8[2]),
+                     "f"(v8[3]), "f"(v8[4]), "f"(v8[5]), "f"(v8[6]), "f"(v8[7])
+                     : "memory");
     }
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = v8[i];
     }
     __device__ __forceinline__ void set(const float (&v)[VEC]) {
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v8[i] = v[i];
     }
 };
 

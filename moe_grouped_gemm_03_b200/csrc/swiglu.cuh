@@ -24,13 +24,19 @@ struct SwigluParams {
     int segment;          // columns of a warp's work, a multiple of 256
 };
 
+// bf16: exp and the reciprocal by their approximating instructions, each within a few 2^-23 (|g| < 20), far below half a
+// step of the result, 2^-8.  exp(-g) of a large negative g is infinite and its reciprocal 0, as it should be.
 template <typename T> __device__ __forceinline__ float sigmoid(float g);
-// bf16: the error of the fast exponential (a few 2^-23 for |g| < 20) is far below half a step of the result's 2^-8
-template <> __device__ __forceinline__ float sigmoid<bf16>(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+template <> __device__ __forceinline__ float sigmoid<bf16>(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 template <> __device__ __forceinline__ float sigmoid<float>(float g) { return 1.f / (1.f + expf(-g)); }
 
 template <typename T, bool FP8, bool BACKWARD, int ROWS>
-__global__ void __launch_bounds__(32 * SWIGLU_WARPS) swiglu_kernel(const SwigluParams p) {
+__global__ void __launch_bounds__(32 * SWIGLU_WARPS, BACKWARD ? 3 : 4) swiglu_kernel(const SwigluParams p) {
     __shared__ int part[SWIGLU_WARPS];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -38,7 +44,7 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS) swiglu_kernel(const SwigluP
     int valid = p.R;  // no padding: rows that the counts cover (negative counts are none)
     if (p.own_kind == OWN_COUNTS) {
         int n = 0;
-        for (int g = threadIdx.x; g < p.G; g += blockDim.x) n = min(n + max(__ldg(p.own + g), 0), p.R);
+        for (int g = threadIdx.x; g < p.G; g += blockDim.x) n = min(n + max(*(p.own + g), 0), p.R);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) n = min(n + __shfl_xor_sync(0xffffffffu, n, d), p.R);
         if (lane == 0) part[warp] = n;
@@ -50,9 +56,9 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS) swiglu_kernel(const SwigluP
     bool owned = false;  // lane r: whether row0 + r is a row of a group
     if (lane < ROWS && row0 + lane < p.R) {
         const int row = row0 + lane;
-        if (p.own_kind == OWN_M_INDICES) owned = __ldg(p.own + row) >= 0;
+        if (p.own_kind == OWN_M_INDICES) owned = *(p.own + row) >= 0;
         else if (p.own_kind == OWN_MASKED)
-            owned = row % p.rows_per_group < __ldg(p.own + row / p.rows_per_group);
+            owned = row % p.rows_per_group < *(p.own + row / p.rows_per_group);
         else owned = row < valid;
     }
     const unsigned live = __ballot_sync(0xffffffffu, owned);
