@@ -223,9 +223,9 @@ DG_EXPORT int dg_fp8_gemm_nt_noalloc(const void *a, const float *sfa, const void
  * of the calls above and take their results).
  *
  * Common to them
- *   - Activations are bf16 or fp32 (dg_dtype), row-major without gaps, their width a multiple of 8.  bf16 tensors, and
- *     e4m3 codes, are 16-byte aligned and fp32 tensors 32-byte aligned (the norms' weights among them); fp32 [T][k] and
- *     [T], gradients of parameters and integers are 4-byte aligned.
+ *   - Activations are bf16 or fp32 (dg_dtype), row-major without gaps, their width a multiple of 8.  bf16 tensors and
+ *     e4m3 codes are 16-byte aligned, fp32 tensors 32-byte aligned (the norms' weights among them); fp32 [T][k] and [T],
+ *     gradients of parameters and integers 4-byte aligned.
  *   - An output that a GEMM takes as its A is e4m3 with scales when its `..._sf` argument is given, else it has the
  *     activations' type and `..._sf` is NULL.  The e4m3 output is laid out as the GEMMs take it: codes [rows][cols]
  *     (cols % 128 == 0) and scales fp32, MN-major [groups][cols/128][dg_get_tma_aligned_size(rows_per_group, 4)],

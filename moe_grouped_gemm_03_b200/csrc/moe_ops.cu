@@ -102,8 +102,8 @@ int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) 
 }
 
 // ----------------------------------------------------------------------------------------- dispatch and combine
-// (out_type: DG_BF16 for e4m3 codes too, whose alignment is the same)
-int check_rows(const void *x, const int *row_of_slot, const void *out, int type, int out_type, int T, int k, int H, int rows) {
+int check_rows(const void *x, const int *row_of_slot, const void *out, const float *out_sf, int type, int T, int k, int H,
+               int rows) {
     // (a tensor without elements may be null)
     if (T > 0 && (!x || !row_of_slot || !out)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
     if (!is_type(type)) return fail(DG_ERR_INVALID_ARG, "unknown element type %d", type);
@@ -112,7 +112,7 @@ int check_rows(const void *x, const int *row_of_slot, const void *out, int type,
     if (k < 1 || k > dg::MAX_TOPK) return fail(DG_ERR_INVALID_ARG, "k=%d must be in [1, %d]", k, dg::MAX_TOPK);
     if (H <= 0) return fail(DG_ERR_INVALID_ARG, "H=%d must be positive", H);
     if (H % dg::VEC) return fail(DG_ERR_ALIGNMENT, "H=%d must be a multiple of %d", H, dg::VEC);
-    if (!vec_aligned(x, type) || !vec_aligned(out, out_type))
+    if (!vec_aligned(x, type) || !vec_aligned(out, out_sf ? DG_BF16 : type))
         return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");
     if (!aligned(row_of_slot, 4)) return fail(DG_ERR_ALIGNMENT, "row_of_slot must be 4-byte aligned");
     return DG_OK;
@@ -150,10 +150,9 @@ int check_items(long long items) {
 }
 
 template <typename T, bool FP8> int launch_permute(dg::RowsParams p, dg_stream_t stream) {
-    constexpr int kSteps = 4;
-    p.segments = (p.H + kSteps * dg::STEP - 1) / (kSteps * dg::STEP);
+    p.segments = (p.H + dg::PERMUTE_COLS - 1) / dg::PERMUTE_COLS;
     if (int rc = check_items(p.T * p.segments)) return rc;
-    return launch("permute launch", dg::permute_kernel<T, FP8, kSteps>, dim3(row_ctas(p.T * p.segments)),
+    return launch("permute launch", dg::permute_kernel<T, FP8>, dim3(row_ctas(p.T * p.segments)),
                   dim3(32 * dg::ROWS_WARPS), 0, 1, stream, p);
 }
 
@@ -166,16 +165,16 @@ template <typename T, bool FP8> int launch_unpermute_backward(const dg::RowsPara
 }
 
 // -------------------------------------------------------------------------------------------------------- SwiGLU
-template <typename T, bool FP8, bool BACKWARD> int launch_swiglu(dg::SwigluParams p, int sms, dg_stream_t stream) {
-    constexpr int kRows = BACKWARD ? 2 : 4;
-    const int ctas = (p.R + kRows * dg::SWIGLU_WARPS - 1) / (kRows * dg::SWIGLU_WARPS);
-    const int steps = (p.I + dg::STEP - 1) / dg::STEP;
-    int splits = (8 * sms + ctas - 1) / ctas;  // columns are split until the SMs are full
-    splits = splits > steps ? steps : splits;
-    const int per = (steps + splits - 1) / splits;
-    p.segment = per * dg::STEP;
-    return launch("swiglu launch", dg::swiglu_kernel<T, FP8, BACKWARD, kRows>, dim3(ctas, (steps + per - 1) / per),
-                  dim3(32 * dg::SWIGLU_WARPS), 0, 1, stream, p);
+template <typename T, bool FP8, bool BACKWARD> int launch_swiglu(dg::SwigluParams p, dg_stream_t stream) {
+    constexpr int kRows = (BACKWARD ? 2 : 4) / (static_cast<int>(sizeof(T)) / 2);
+    const int steps = (p.I + dg::STEP_COLS - 1) / dg::STEP_COLS;
+    for (p.across = 1; p.across < dg::SWIGLU_WARPS && p.across < steps;) p.across *= 2;
+    // two turns of the CTA's warps (I = 2048: 8 rows; 16 or 32 leave short calls too few CTAs, 4 are too short a life)
+    p.cta_rows = 2 * kRows * dg::SWIGLU_WARPS / p.across;
+    if (p.cta_rows > 32) p.cta_rows = 32;
+    return launch("swiglu launch", dg::swiglu_kernel<T, FP8, BACKWARD, kRows>,
+                  dim3((p.R + p.cta_rows - 1) / p.cta_rows, (steps + p.across - 1) / p.across), dim3(32 * dg::SWIGLU_WARPS), 0,
+                  1, stream, p);
 }
 
 int swiglu_call(dg::SwigluParams p, int type, bool backward, const int *m_indices, const int *counts, const int *masked_m,
@@ -186,7 +185,8 @@ int swiglu_call(dg::SwigluParams p, int type, bool backward, const int *m_indice
     if (p.I <= 0 || p.I > (1 << 24)) return fail(DG_ERR_INVALID_ARG, "I=%d must be in [1, 2^24]", p.I);
     if (p.I % dg::VEC) return fail(DG_ERR_ALIGNMENT, "I=%d must be a multiple of %d", p.I, dg::VEC);
     if (out_sf && p.I % 128) return fail(DG_ERR_ALIGNMENT, "I=%d must be a multiple of 128 for an e4m3 output", p.I);
-    if (!vec_aligned(p.gate_up, type) || !vec_aligned(p.out, out_sf ? DG_BF16 : type) || !vec_aligned(p.d_out, type))
+    if (!vec_aligned(p.gate_up, type) || !vec_aligned(p.out, out_sf ? DG_BF16 : type) ||
+        !vec_aligned(p.d_out, type))
         return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");
     if ((m_indices != nullptr) + (counts != nullptr) + (masked_m != nullptr) > 1)
         return fail(DG_ERR_INVALID_ARG, "at most one of m_indices, counts and masked_m may be given");
@@ -202,11 +202,11 @@ int swiglu_call(dg::SwigluParams p, int type, bool backward, const int *m_indice
     int device, sms;
     if (int rc = dg::current_device(device, sms)) return rc;
     if (type == DG_BF16) {
-        if (backward) return out_sf ? launch_swiglu<bf16, true, true>(p, sms, stream) : launch_swiglu<bf16, false, true>(p, sms, stream);
-        return out_sf ? launch_swiglu<bf16, true, false>(p, sms, stream) : launch_swiglu<bf16, false, false>(p, sms, stream);
+        if (backward) return out_sf ? launch_swiglu<bf16, true, true>(p, stream) : launch_swiglu<bf16, false, true>(p, stream);
+        return out_sf ? launch_swiglu<bf16, true, false>(p, stream) : launch_swiglu<bf16, false, false>(p, stream);
     }
-    if (backward) return out_sf ? launch_swiglu<float, true, true>(p, sms, stream) : launch_swiglu<float, false, true>(p, sms, stream);
-    return out_sf ? launch_swiglu<float, true, false>(p, sms, stream) : launch_swiglu<float, false, false>(p, sms, stream);
+    if (backward) return out_sf ? launch_swiglu<float, true, true>(p, stream) : launch_swiglu<float, false, true>(p, stream);
+    return out_sf ? launch_swiglu<float, true, false>(p, stream) : launch_swiglu<float, false, false>(p, stream);
 }
 
 // --------------------------------------------------------------------------------------------------------- norms
@@ -222,12 +222,12 @@ int check_norm(const dg::NormParams &p, int x_type, int y_type, int param_type) 
     if (p.T != 0 && (p.gate_kind < dg::GATE_NONE || p.gate_kind > dg::GATE_TOKEN))
         return fail(DG_ERR_INVALID_ARG, "gate_kind must be 0 without a gate, 1 ([H]) or 2 ([T][H]) with one");
     const int gate_type = p.gate_kind == dg::GATE_ROW ? param_type : y_type;
-    if (!vec_aligned(p.x, x_type) || !vec_aligned(p.x_out, x_type) || !vec_aligned(p.d_x_out, x_type) ||
-        !vec_aligned(p.d_x, x_type) || !vec_aligned(p.y, y_type) || !vec_aligned(p.d_h, y_type) ||
-        !vec_aligned(p.d_y, y_type) || !vec_aligned(p.d_gate_token, y_type) ||
-        !vec_aligned(p.h, p.sf.sf ? static_cast<int>(DG_BF16) : y_type) || !vec_aligned(p.w, param_type) ||
-        !vec_aligned(p.w_post, param_type) || !vec_aligned(p.gate, gate_type))
-        return fail(DG_ERR_ALIGNMENT, "tensors of the norms must be 16-byte (fp32: 32-byte) aligned");
+    auto bad = [&](const void *q, int type) { return !vec_aligned(q, type); };
+    if (bad(p.x, x_type) || bad(p.x_out, x_type) || bad(p.d_x_out, x_type) || bad(p.d_x, x_type) || bad(p.y, y_type) ||
+        bad(p.d_h, y_type) || bad(p.d_y, y_type) || bad(p.d_gate_token, y_type) || bad(p.w, param_type) ||
+        bad(p.w_post, param_type) || bad(p.gate, gate_type) || !vec_aligned(p.h, p.sf.sf ? DG_BF16 : y_type))
+        return fail(DG_ERR_ALIGNMENT,
+                    "tensors of the norms must be 16-byte (fp32: 32-byte) aligned");
     if (!aligned(p.rstd, 4) || !aligned(p.rstd_post, 4))
         return fail(DG_ERR_ALIGNMENT, "rstd and rstd_post must be 4-byte aligned");
     return DG_OK;
@@ -239,19 +239,47 @@ int gate_of(const void *gate, int kind) {
     return kind == dg::GATE_ROW || kind == dg::GATE_TOKEN ? kind : -1;
 }
 
-// Threads of a CTA and vectors of a thread for a row of H elements.
-void row_shape(int H, int &threads, int &iters) {
-    const int vecs = H / dg::VEC;
-    iters = vecs <= dg::NORM_MAX_THREADS ? 1 : vecs <= 2 * dg::NORM_MAX_THREADS ? 2 : 4;
-    threads = ((vecs + iters - 1) / iters + 31) / 32 * 32;
+// Launch of the kernels whose rows go through shared memory: CTAs of a vector a thread, as many an SM as `per_sm` and the
+// shared memory allow, with up to four stages each; one CTA fewer where that leaves no second stage.
+struct NormShape {
+    int threads, ctas, stages;
+    size_t smem;
+};
+
+NormShape norm_shape(const dg::NormParams &p, int stage_units, int per_sm, int sms) {
+    NormShape s{};
+    s.threads = (p.H / dg::VEC + 31) / 32 * 32;
+    const int unit = 16 * s.threads, param_bytes = dg::norm_param_units(p.param_f32, p.gate_kind) * unit, stage_bytes = stage_units * unit;
+    auto stages = [&](int n) { return (dg::NORM_SHARED_BYTES / n - 1024 - param_bytes) / stage_bytes; };
+    while (per_sm > 1 && stages(per_sm) < 2) --per_sm;
+    s.ctas = p.T < per_sm * sms ? p.T : per_sm * sms;
+    s.stages = stages(per_sm);
+    const int rows = (p.T + s.ctas - 1) / s.ctas;  // (of a CTA: more stages would stay empty)
+    s.stages = s.stages > dg::NORM_MAX_STAGES ? dg::NORM_MAX_STAGES : s.stages < 1 ? 1 : s.stages;
+    s.stages = s.stages > rows ? rows : s.stages;
+    s.smem = static_cast<size_t>(param_bytes) + static_cast<size_t>(s.stages) * stage_bytes;
+    return s;
 }
 
-template <typename X, typename Y> int launch_norm(const dg::NormParams &p, dg_stream_t stream) {
-    int threads, iters;
-    row_shape(p.H, threads, iters);
-    auto kernel = iters == 1 ? dg::rms_norm_kernel<X, Y, 1>
-                             : iters == 2 ? dg::rms_norm_kernel<X, Y, 2> : dg::rms_norm_kernel<X, Y, 4>;
+int launch_norm_ring(const char *name, void (*kernel)(dg::NormParams), const dg::NormParams &p, const NormShape &s,
+                     dg_stream_t stream) {
+    cudaError_t e;
+    // (48 KB without being told so, the kernel's static 256 bytes among them)
+    if (s.smem > 47 * 1024 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        static_cast<int>(s.smem))) != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute (norm)");
+    return launch(name, kernel, dim3(s.ctas), dim3(s.threads), s.smem, 1, stream, p);
+}
+
+template <typename X, typename Y, bool FP8> int launch_norm(const dg::NormParams &p, int sms, dg_stream_t stream) {
+    const int iters = p.T <= sms && p.H <= dg::VEC * dg::NORM_MAX_THREADS ? 1 : 4;
+    const int threads = ((p.H / dg::VEC + iters - 1) / iters + 31) / 32 * 32;
+    auto kernel = iters == 1 ? dg::rms_norm_kernel<X, Y, FP8, 1>
+                             : iters == 2 ? dg::rms_norm_kernel<X, Y, FP8, 2> : dg::rms_norm_kernel<X, Y, FP8, 4>;
     return launch("norm launch", kernel, dim3(static_cast<unsigned>(p.T)), dim3(threads), 0, 1, stream, p);
+}
+template <typename X, typename Y> int launch_norm(const dg::NormParams &p, int sms, dg_stream_t stream) {
+    return p.sf.sf ? launch_norm<X, Y, true>(p, sms, stream) : launch_norm<X, Y, false>(p, sms, stream);
 }
 
 int norm_call(const dg::NormParams &p, int x_type, int y_type, int param_type, dg_stream_t stream) {
@@ -259,16 +287,29 @@ int norm_call(const dg::NormParams &p, int x_type, int y_type, int param_type, d
     if (p.T == 0) return DG_OK;
     int device, sms;
     if (int rc = dg::current_device(device, sms)) return rc;
-    if (x_type == DG_BF16) return launch_norm<bf16, bf16>(p, stream);
-    return y_type == DG_BF16 ? launch_norm<float, bf16>(p, stream) : launch_norm<float, float>(p, stream);
+    if (x_type == DG_BF16) return launch_norm<bf16, bf16>(p, sms, stream);
+    return y_type == DG_BF16 ? launch_norm<float, bf16>(p, sms, stream) : launch_norm<float, float>(p, sms, stream);
 }
 
-template <typename X, typename Y> int launch_norm_backward(const dg::NormParams &p, int ctas, dg_stream_t stream) {
-    int threads, iters;
-    row_shape(p.H, threads, iters);
-    auto kernel = iters == 1 ? dg::rms_norm_backward_kernel<X, Y, 1>
-                             : iters == 2 ? dg::rms_norm_backward_kernel<X, Y, 2> : dg::rms_norm_backward_kernel<X, Y, 4>;
-    return launch("norm gradient launch", kernel, dim3(ctas), dim3(threads), 0, 1, stream, p);
+// (wide rows: one CTA an SM)
+template <typename X, typename Y> NormShape norm_backward_shape(const dg::NormParams &p, int sms) {
+    if (p.H > dg::NORM_RING_H) return NormShape{dg::NORM_WIDE_THREADS, p.T < sms ? p.T : sms, 0, 0};
+    const int units = dg::norm_stage_units(dg::Raw<X>::UNITS, dg::Raw<Y>::UNITS, p.w != nullptr, p.y != nullptr,
+                                           p.gate_kind == dg::GATE_TOKEN);
+    const int threads = (p.H / dg::VEC + 31) / 32 * 32;
+    // at 64 registers; more than 8 CTAs an SM would add more to the sums over the CTAs than they save
+    const int per_sm = dg::NORM_MAX_THREADS / threads;
+    return norm_shape(p, units, per_sm > 8 ? 8 : per_sm, sms);
+}
+
+template <typename X, typename Y> int launch_norm_backward(const dg::NormParams &p, const NormShape &s, dg_stream_t stream) {
+    if (p.H > dg::NORM_RING_H)
+        return launch("norm gradient launch", dg::rms_norm_backward_wide_kernel<X, Y, 4>, dim3(s.ctas), dim3(s.threads), 0, 1,
+                      stream, p);
+    auto kernel = p.gate_kind == dg::GATE_NONE  ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE>
+                  : p.gate_kind == dg::GATE_ROW ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_ROW>
+                                                : dg::rms_norm_backward_kernel<X, Y, dg::GATE_TOKEN>;
+    return launch_norm_ring("norm gradient launch", kernel, p, s, stream);
 }
 
 int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type, float *d_w, float *d_w_post,
@@ -286,20 +327,24 @@ int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type,
     }
     int device, sms;
     if (int rc = dg::current_device(device, sms)) return rc;
-    const int ctas = p.T < 2 * sms ? p.T : 2 * sms;
+    const NormShape shape = x_type == DG_BF16   ? norm_backward_shape<bf16, bf16>(p, sms)
+                            : y_type == DG_BF16 ? norm_backward_shape<float, bf16>(p, sms)
+                                                : norm_backward_shape<float, float>(p, sms);
+    const int ctas = shape.ctas;
+    p.stages = shape.stages;
     cudaMemPool_t pool;
     if (int rc = dg::scratch_pool(device, pool)) return rc;
     void *partial = nullptr;
     e = cudaMallocFromPoolAsync(&partial, sizeof(float) * 3 * p.H * static_cast<size_t>(ctas), pool, s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync (parameter gradients)");
     p.partial = static_cast<float *>(partial);
-    int rc = x_type == DG_BF16   ? launch_norm_backward<bf16, bf16>(p, ctas, stream)
-             : y_type == DG_BF16 ? launch_norm_backward<float, bf16>(p, ctas, stream)
-                                 : launch_norm_backward<float, float>(p, ctas, stream);
+    int rc = x_type == DG_BF16   ? launch_norm_backward<bf16, bf16>(p, shape, stream)
+             : y_type == DG_BF16 ? launch_norm_backward<float, bf16>(p, shape, stream)
+                                 : launch_norm_backward<float, float>(p, shape, stream);
     if (rc == DG_OK && (d_w || d_w_post || d_gate_row))
         rc = launch("norm gradient sum launch", dg::rms_norm_sum_kernel,
-                    dim3((p.H + dg::NORM_SUM_COLS - 1) / dg::NORM_SUM_COLS, 3), dim3(dg::NORM_SUM_COLS, dg::NORM_SUM_PARTS), 0,
-                    1, stream, static_cast<const float *>(p.partial), ctas, p.H, d_w, d_w_post, d_gate_row);
+                    dim3((p.H + 4 * dg::NORM_SUM_LANES - 1) / (4 * dg::NORM_SUM_LANES), 3),
+                    dim3(dg::NORM_SUM_LANES, dg::NORM_SUM_PARTS), 0, 1, stream, static_cast<const float *>(p.partial), ctas, p.H, d_w, d_w_post, d_gate_row);
     e = cudaFreeAsync(partial, s);
     if (rc == DG_OK && e != cudaSuccess) rc = cuda_fail(e, "cudaFreeAsync (parameter gradients)");
     return rc;
@@ -366,7 +411,7 @@ int dg_moe_permute(const void *x, int type, const int *row_of_slot, int T, int k
                    void *out, float *out_sf, dg_stream_t stream) {
     dg::RowsParams p{};
     if (rows == 0) T = 0;  // nowhere to write
-    if (int rc = check_rows(x, row_of_slot, out, type, out_sf ? DG_BF16 : type, T, k, H, rows)) return rc;
+    if (int rc = check_rows(x, row_of_slot, out, out_sf, type, T, k, H, rows)) return rc;
     if (int rc = scale_layout(p.sf, out_sf, rows, rows_per_group, H)) return rc;
     if (T == 0) return DG_OK;
     if (int rc = rows_params(p, x, row_of_slot, T, k, H, rows, out)) return rc;
@@ -378,7 +423,7 @@ int dg_moe_unpermute(const void *rows_in, int type, const int *row_of_slot, cons
                      int rows, void *out, dg_stream_t stream) {
     dg::RowsParams p{};
     if (rows == 0) rows_in = out;  // (no row is read)
-    if (int rc = check_rows(rows_in, row_of_slot, out, type, type, T, k, H, rows)) return rc;
+    if (int rc = check_rows(rows_in, row_of_slot, out, nullptr, type, T, k, H, rows)) return rc;
     if (!aligned(weights, 4)) return fail(DG_ERR_ALIGNMENT, "weights must be 4-byte aligned");
     if (T == 0) return DG_OK;
     if (int rc = rows_params(p, rows_in, row_of_slot, T, k, H, rows, out)) return rc;
@@ -395,7 +440,7 @@ int dg_moe_unpermute_backward(const void *d_out, const void *rows_in, int type, 
                               float *d_rows_sf, float *d_weights, dg_stream_t stream) {
     dg::RowsParams p{};
     if (rows == 0) rows_in = d_rows = const_cast<void *>(d_out);  // (no row is read or written)
-    if (int rc = check_rows(rows_in, row_of_slot, d_rows, type, d_rows_sf ? DG_BF16 : type, T, k, H, rows)) return rc;
+    if (int rc = check_rows(rows_in, row_of_slot, d_rows, d_rows_sf, type, T, k, H, rows)) return rc;
     if (T > 0 && (!d_out || !weights || !d_weights)) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
     if (!vec_aligned(d_out, type)) return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");
     if (!aligned(weights, 4) || !aligned(d_weights, 4))

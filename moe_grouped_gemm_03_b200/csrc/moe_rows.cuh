@@ -37,10 +37,13 @@ __device__ __forceinline__ int slot_row(const RowsParams &p, long long token, in
     return row < p.rows ? row : -1;
 }
 
-// A warp takes STEPS * 256 columns of a token: all loads first, then each block is quantised once, then the slots in turn,
-// so that a slot's address is made once for all of its stores.
-template <typename T, bool FP8, int STEPS>
+constexpr int PERMUTE_COLS = 1024;  // of a token, a warp's work
+
+// All loads first, then each block is quantised once, then the slots in turn, so that a slot's address is made once for all
+// of its stores.
+template <typename T, bool FP8>
 __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsParams p) {
+    constexpr int kSteps = PERMUTE_COLS / STEP;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -50,35 +53,35 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsPara
     const int row = slot_row(p, token, lane);
     const unsigned live = __ballot_sync(0xffffffffu, row >= 0);
     if (!live) return;
-    const int begin = static_cast<int>(item - token * p.segments) * STEPS * STEP + lane * VEC;
+    const int begin = static_cast<int>(item - token * p.segments) * PERMUTE_COLS + lane * VEC;
     const T *x = static_cast<const T *>(p.x) + token * p.H;
-    Raw8<T> r[STEPS];
+    Raw<T> r[kSteps];
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j)
+    for (int j = 0; j < kSteps; ++j)
         if (begin + j * STEP < p.H) r[j].load(x + begin + j * STEP);
     if constexpr (FP8) {
-        uint2 q[STEPS];
-        float scale[STEPS];
+        uint2 q[kSteps];
+        float scale[kSteps];
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
+        for (int j = 0; j < kSteps; ++j) {
             float v[VEC] = {};
             if (begin + j * STEP < p.H) r[j].get(v);
-            q[j] = quantise8(v, block_amax(v), scale[j]);
+            q[j] = quantise(v, block_amax(v), scale[j]);
         }
         for (unsigned m = live; m; m &= m - 1) {
             const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
             uint8_t *out = static_cast<uint8_t *>(p.out) + at * p.H + begin;
 #pragma unroll
-            for (int j = 0; j < STEPS; ++j)
+            for (int j = 0; j < kSteps; ++j)
                 if (begin + j * STEP < p.H) *reinterpret_cast<uint2 *>(out + j * STEP) = q[j];
         }
-        // lanes s and 16 + s of the warp write slot s's scales of a step's two blocks
+        // lane s of each block's lanes writes slot s's scale of the block, 16 slots at a time
         for (int s = 0; s < p.k; s += BLOCK_LANES) {
-            const int at = __shfl_sync(0xffffffffu, row, s + (lane & 15));
+            const int at = __shfl_sync(0xffffffffu, row, s + (lane & (BLOCK_LANES - 1)));
             if (at < 0) continue;
             float *sf = p.sf.at(at, begin >> 7);
 #pragma unroll
-            for (int j = 0; j < STEPS; ++j)
+            for (int j = 0; j < kSteps; ++j)
                 if (begin + j * STEP < p.H) sf[static_cast<long long>(j) * (STEP / 128) * p.sf.ld] = scale[j];
         }
     } else {
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsPara
             const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
             T *out = static_cast<T *>(p.out) + at * p.H + begin;
 #pragma unroll
-            for (int j = 0; j < STEPS; ++j)
+            for (int j = 0; j < kSteps; ++j)
                 if (begin + j * STEP < p.H) r[j].store(out + j * STEP);
         }
     }
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) unpermute_kernel(const RowsPa
     float acc[VEC] = {};
     unsigned m = __ballot_sync(0xffffffffu, row >= 0);
     while (m) {
-        Raw8<T> r[U];
+        Raw<T> r[U];
         float weight[U];
         int n = 0;
 #pragma unroll
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) unpermute_kernel(const RowsPa
                 for (int i = 0; i < VEC; ++i) acc[i] = fmaf(weight[u], v[i], acc[i]);
             }
     }
-    if (in) store8(static_cast<T *>(p.out) + token * p.H + col, acc);
+    if (in) store_vec(static_cast<T *>(p.out) + token * p.H + col, acc);
 }
 
 constexpr int GRAD_SLOTS = 8;       // slots of a token at a time
@@ -151,22 +154,28 @@ __global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel
     const T *rows = static_cast<const T *>(p.x);
     for (int first = 0; first < p.k; first += GRAD_SLOTS) {
         int at[GRAD_SLOTS];
-        float weight[GRAD_SLOTS], acc[GRAD_SLOTS] = {};
+        float weight[GRAD_SLOTS], acc[GRAD_SLOTS][2] = {};
 #pragma unroll
         for (int u = 0; u < GRAD_SLOTS; ++u) {
             at[u] = __shfl_sync(0xffffffffu, row, (first + u) & 31);
             if (first + u >= p.k) at[u] = -1;
             weight[u] = __shfl_sync(0xffffffffu, w, (first + u) & 31);
         }
+        // lanes u and 16 + u write slot first + u's scales: this is where the row's first one goes
+        float *sf = nullptr;
+        if constexpr (FP8) {
+            const int mine = __shfl_sync(0xffffffffu, row, (first + (lane & 15)) & 31);
+            if ((lane & 15) < GRAD_SLOTS && first + (lane & 15) < p.k && mine >= 0) sf = p.sf.at(mine, 0);
+        }
         for (int base = warp * STEP; base < p.H; base += warps * STEP) {
             const int col = base + lane * VEC;
             const bool in = col < p.H;
-            Raw8<T> r[GRAD_SLOTS];
+            Raw<T> r[GRAD_SLOTS];
 #pragma unroll
             for (int u = 0; u < GRAD_SLOTS; ++u)
                 if (at[u] >= 0 && in) r[u].load(rows + static_cast<long long>(at[u]) * p.H + col);
             float d[VEC] = {}, amax = 0.f, keep = 0.f;
-            if (in) load8(d_out + col, d);
+            if (in) load_vec(d_out + col, d);
             if constexpr (FP8) amax = block_amax(d);
 #pragma unroll
             for (int u = 0; u < GRAD_SLOTS; ++u)
@@ -174,33 +183,31 @@ __global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel
                     if (in) {
                         float v[VEC];
                         r[u].get(v);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) acc[u] = fmaf(d[i], v[i], acc[u]);
+                        dot_vec(acc[u], d, v);
                     }
                     float g[VEC];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) g[i] = weight[u] * d[i];
+                    for (int i = 0; i < VEC; ++i) g[i] = d[i];
+                    mul_vec(g, weight[u]);
                     if constexpr (FP8) {
                         // rounding keeps order: the largest of the rounded products is the product of the largest
                         float scale;
-                        const uint2 q = quantise8(g, fabsf(weight[u]) * amax, scale);
+                        const uint2 q = quantise(g, fabsf(weight[u]) * amax, scale);
                         if ((lane & 15) == u) keep = scale;
                         if (in)
                             *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) +
                                                        static_cast<long long>(at[u]) * p.H + col) = q;
                     } else if (in) {
-                        store8(static_cast<T *>(p.out) + static_cast<long long>(at[u]) * p.H + col, g);
+                        store_vec(static_cast<T *>(p.out) + static_cast<long long>(at[u]) * p.H + col, g);
                     }
                 }
             if constexpr (FP8) {
-                const int mine = __shfl_sync(0xffffffffu, row, (first + (lane & 15)) & 31);
-                if (in && (lane & 15) < GRAD_SLOTS && first + (lane & 15) < p.k && mine >= 0)
-                    *p.sf.at(mine, col >> 7) = keep;
+                if (in && sf) sf[static_cast<long long>(col >> 7) * p.sf.ld] = keep;
             }
         }
 #pragma unroll
         for (int u = 0; u < GRAD_SLOTS; ++u) {
-            float sum = acc[u];
+            float sum = acc[u][0] + acc[u][1];
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (lane == 0) part[u][warp] = sum;

@@ -9,15 +9,23 @@
 //   d_n  = alpha * gate * d_x,                                  d_gate = alpha * n * d_x (summed over t for [H])
 //   d_y  = r_y * (w_post d_n - y r_y^2 mean(w_post d_n y)),     d_w_post = sum_t d_n y r_y
 //
-// Bound by HBM: one pass over every tensor.  A row stays in the registers of one CTA between its sums, which are kept
-// in fp32, as are x' before h and everything else until its one rounding.
+// Bound by HBM: one pass over every tensor.  A row belongs to one CTA, a thread to eight of its columns.  Between a row's
+// loads and its stores lie one or two sums over the CTA, so a CTA that loads, sums and stores in turn leaves the memory
+// idle most of the time.  The CTAs therefore stay (as many as fit on the SMs, each taking every CTAs-th row) and copy
+// their next rows to shared memory ahead of use; the parameters lie there too, copied once.  Every thread copies what it
+// will read itself, so no barrier goes with the copies.  Rows of more than 8192 columns do not fit and go without.
+// Sums are fp32, as are x' before h and everything else until its one rounding.
 #pragma once
 #include "rowwise.cuh"
 
 namespace dg {
 
 constexpr int NORM_MAX_H = 16384;
-constexpr int NORM_MAX_THREADS = 512;
+constexpr int NORM_MAX_THREADS = 1024;                  // of a CTA whose rows go through shared memory, a vector each
+constexpr int NORM_RING_H = NORM_MAX_THREADS * VEC;     // widest row of such a CTA
+constexpr int NORM_WIDE_THREADS = 512;                  // of a CTA for wider rows
+constexpr int NORM_MAX_STAGES = 4;
+constexpr int NORM_SHARED_BYTES = 226 * 1024;           // of an SM, for the CTAs' parameters and stages
 enum GateKind { GATE_NONE = 0, GATE_ROW = 1, GATE_TOKEN = 2 };
 
 struct NormParams {
@@ -31,11 +39,12 @@ struct NormParams {
     float *partial;                    // gradient: [CTAs][3][H]: d_w, d_w_post, d_gate [H]
     float alpha, eps;
     int T, H, param_f32, gate_kind;
+    int stages;                        // rows of a CTA under way in shared memory
 };
 
-__device__ __forceinline__ void load_param8(const void *p, int f32, int i, float (&v)[VEC]) {
-    if (f32) load8(static_cast<const float *>(p) + i, v);
-    else load8(static_cast<const bf16 *>(p) + i, v);
+__device__ __forceinline__ void load_param(const void *p, int f32, int i, float (&v)[VEC]) {
+    if (f32) load_vec(static_cast<const float *>(p) + i, v);
+    else load_vec(static_cast<const bf16 *>(p) + i, v);
 }
 
 // Sum over the CTA, the same in every thread.  `part` is read until the next barrier: two buffers in turn.
@@ -43,6 +52,7 @@ __device__ __forceinline__ float cta_sum(float v, float *part) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (warps == 1) return v;
     if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     v = lane < warps ? part[lane] : 0.f;
@@ -51,213 +61,402 @@ __device__ __forceinline__ float cta_sum(float v, float *part) {
     return v;
 }
 
-template <typename X, typename Y, int ITERS>
-__global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_kernel(const NormParams p) {
+// A thread's vectors in shared memory: the parameters (w, w_post, a gate [H]) and the stages of a row's tensors, each vector
+// of T as Raw<T>::UNITS units of 16 bytes, a unit of all threads side by side.
+struct NormSlots {
+    uint4 *mine;
+    int stage;  // first unit of the stage in use
+
+    __device__ __forceinline__ uint4 *unit(int n) const { return mine + n * static_cast<int>(blockDim.x); }
+    template <typename T> __device__ __forceinline__ void copy(int n, const void *src, long long i) const {
+        Raw<T>::load_async(unit(n), blockDim.x, static_cast<const T *>(src) + i);
+    }
+    template <typename T> __device__ __forceinline__ void get(int n, float (&v)[VEC]) const {
+        Raw<T> raw;
+        raw.load_shared(unit(n), blockDim.x);
+        raw.get(v);
+    }
+    // parameter number i
+    __device__ __forceinline__ void copy_param(int i, const void *src, int f32, int col) const {
+        if (f32) copy<float>(2 * i, src, col);
+        else copy<bf16>(i, src, col);
+    }
+    __device__ __forceinline__ void get_param(int i, int f32, float (&v)[VEC]) const {
+        if (f32) get<float>(2 * i, v);
+        else get<bf16>(i, v);
+    }
+};
+
+// Waits until the oldest of `stages` groups of copies has come.
+__device__ __forceinline__ void wait_stage(int stages) {
+    switch (stages) {
+        case 1: copy_async_wait<0>(); break;
+        case 2: copy_async_wait<1>(); break;
+        case 3: copy_async_wait<2>(); break;
+        default: copy_async_wait<3>(); break;
+    }
+}
+
+// Units of a thread: parameters (w, w_post and a gate [H]), and one stage.
+__host__ __device__ constexpr int norm_param_units(int param_f32, int gate_kind) {
+    return (gate_kind == GATE_ROW ? 3 : 2) * (param_f32 ? 2 : 1);
+}
+__host__ __device__ constexpr int norm_stage_units(int x, int y, bool has_w, bool has_y, bool gate_token) {
+    return x + (has_w ? x + y : 0) + (has_y ? y : 0) + (gate_token ? y : 0);
+}
+
+// The parameters' sums over the CTA's rows stay in registers and go to `partial` once.
+template <typename X, typename Y, int GATE>
+__global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(const NormParams p) {
+    extern __shared__ uint4 norm_smem[];
+    __shared__ float part[2][32];
+    constexpr int UX = Raw<X>::UNITS, UY = Raw<Y>::UNITS;
+    const int col = threadIdx.x * VEC;
+    const bool in = col < p.H, has_y = p.y != nullptr, has_w = p.w != nullptr;
+    const float inv_h = 1.f / p.H;
+    const int first_stage = norm_param_units(p.param_f32, GATE);
+    const int stage_units = norm_stage_units(UX, UY, has_w, has_y, GATE == GATE_TOKEN);
+    const int y_unit = UX + (has_w ? UX + UY : 0);  // units of a stage: d_x_out, x', d_h, y, gate
+    NormSlots s{norm_smem + threadIdx.x, first_stage};
+    grid_dependency_wait();
+    grid_launch_dependents();
+    auto fill = [&](long long row, int stage) {
+        if (in && row < p.T) {
+            const long long at = row * p.H + col;
+            if (has_w) {
+                s.copy<X>(stage + UX, p.x, at);
+                s.copy<Y>(stage + 2 * UX, p.d_h, at);
+            }
+            if (p.d_x_out) s.copy<X>(stage, p.d_x_out, at);
+            if (has_y) s.copy<Y>(stage + y_unit, p.y, at);
+            if (GATE == GATE_TOKEN) s.copy<Y>(stage + y_unit + UY, p.gate, at);
+        }
+        copy_async_commit();
+    };
+    if (in) {
+        if (has_w) s.copy_param(0, p.w, p.param_f32, col);
+        if (p.w_post) s.copy_param(1, p.w_post, p.param_f32, col);
+        if (GATE == GATE_ROW) s.copy_param(2, p.gate, p.param_f32, col);
+    }
+    for (int i = 0; i < p.stages; ++i) fill(blockIdx.x + static_cast<long long>(i) * gridDim.x, first_stage + i * stage_units);
+    float sum_w[VEC] = {}, sum_post[VEC] = {}, sum_gate[VEC] = {};
+    float r = 0.f, r_post = 1.f;  // of the row to come, loaded a row ahead
+    if (has_w) r = p.rstd[blockIdx.x];
+    if (p.w_post) r_post = p.rstd_post[blockIdx.x];
+    for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
+        const long long at = static_cast<long long>(row) * p.H + col;
+        const int next = row + static_cast<int>(gridDim.x) < p.T ? row + gridDim.x : row;
+        float r_next = 0.f, r_post_next = 1.f;
+        if (has_w) r_next = p.rstd[next];
+        if (p.w_post) r_post_next = p.rstd_post[next];
+        wait_stage(p.stages);
+        float dx[VEC] = {}, t[VEC] = {}, c[VEC] = {};
+        if (has_w) {
+            float sum[2] = {};
+            if (in) {
+                s.get<X>(s.stage + UX, t);
+                s.get<Y>(s.stage + 2 * UX, dx);
+                s.get_param(0, p.param_f32, c);
+                mul_vec(t, r);
+                fma_vec(sum_w, dx, t);
+                mul_vec(dx, c);
+                dot_vec(sum, dx, t);  // dx: w d_h, t: x' r
+            }
+            const float mean = cta_sum(sum[0] + sum[1], part[0]) * inv_h;
+            fma_vec(dx, t, -mean);
+            if (p.d_x_out) {
+                if (in) s.get<X>(s.stage, t);
+                fma_vec(t, dx, r);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) dx[i] = t[i];
+            } else {
+                mul_vec(dx, r);
+            }
+        } else if (in) {
+            s.get<X>(s.stage, dx);
+        }
+        if (in) store_vec(static_cast<X *>(p.d_x) + at, dx);
+        if (has_y) {
+            float sum[2] = {};
+            if (in) {
+                s.get<Y>(s.stage + y_unit, t);
+                mul_vec(t, r_post);
+                mul_vec(dx, p.alpha);
+                if (GATE != GATE_NONE) {  // d_gate = alpha d_x n, n = t w_post
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) c[i] = t[i];
+                    mul_vec(c, dx);
+                    if (p.w_post) {
+                        float post[VEC];
+                        s.get_param(1, p.param_f32, post);
+                        mul_vec(c, post);
+                    }
+                    if (GATE == GATE_ROW) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) sum_gate[i] += c[i];
+                        s.get_param(2, p.param_f32, c);
+                    } else {
+                        store_vec(static_cast<Y *>(p.d_gate_token) + at, c);
+                        s.get<Y>(s.stage + y_unit + UY, c);
+                    }
+                    mul_vec(dx, c);
+                }
+                if (p.w_post) {
+                    fma_vec(sum_post, dx, t);
+                    s.get_param(1, p.param_f32, c);
+                    mul_vec(dx, c);
+                    dot_vec(sum, dx, t);
+                }
+            }
+            if (p.w_post) {
+                const float mean = cta_sum(sum[0] + sum[1], part[1]) * inv_h;
+                fma_vec(dx, t, -mean);
+                mul_vec(dx, r_post);
+            }
+            if (in) store_vec(static_cast<Y *>(p.d_y) + at, dx);
+        }
+        fill(row + static_cast<long long>(p.stages) * gridDim.x, s.stage);
+        s.stage += stage_units;
+        if (s.stage == first_stage + p.stages * stage_units) s.stage = first_stage;
+        r = r_next;
+        r_post = r_post_next;
+        if (!(has_w && p.w_post)) __syncthreads();
+    }
+    if (!in) return;
+    float *partial = p.partial + static_cast<long long>(blockIdx.x) * 3 * p.H + col;
+    if (has_w) store_vec(partial, sum_w);
+    if (p.w_post) store_vec(partial + p.H, sum_post);
+    if (GATE == GATE_ROW) store_vec(partial + 2 * p.H, sum_gate);
+}
+
+// One CTA a row, which waits for the sums in registers; ITERS vectors a thread.
+template <typename X, typename Y, bool FP8, int ITERS>
+__global__ void __launch_bounds__(ITERS == 1 ? NORM_MAX_THREADS : NORM_MAX_H / 32) rms_norm_kernel(const NormParams p) {
     __shared__ float part[2][32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int row = blockIdx.x;
     const long long at = static_cast<long long>(row) * p.H;
-    float x[ITERS][VEC];
+    const float inv_h = 1.f / p.H;
+    Raw<X> rx[ITERS];
+    Raw<Y> ry[ITERS];
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
         const int col = (j * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[j][i] = 0.f;
-        if (col < p.H) load8(static_cast<const X *>(p.x) + at + col, x[j]);
+        if (col < p.H) {
+            rx[j].load(static_cast<const X *>(p.x) + at + col);
+            if (p.y) ry[j].load(static_cast<const Y *>(p.y) + at + col);
+        }
     }
-    if (p.y) {
-        float n[ITERS][VEC];
-        float sum = 0.f;
+    float r_post = 1.f;
+    if (p.w_post) {
+        float sum[2] = {};
 #pragma unroll
-        for (int j = 0; j < ITERS; ++j) {
-            const int col = (j * blockDim.x + threadIdx.x) * VEC;
+        for (int j = 0; j < ITERS; ++j)
+            if ((j * blockDim.x + threadIdx.x) * VEC < p.H) {
+                float n[VEC];
+                ry[j].get(n);
+                dot_vec(sum, n, n);
+            }
+        r_post = rsqrtf(fmaf(cta_sum(sum[0] + sum[1], part[0]), inv_h, p.eps));
+        if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[row] = r_post;
+    }
+    float x[ITERS][VEC], sum[2] = {};
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) n[j][i] = 0.f;
-            if (col < p.H) load8(static_cast<const Y *>(p.y) + at + col, n[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) sum = fmaf(n[j][i], n[j][i], sum);
-        }
-        float r = 1.f;
-        if (p.w_post) {
-            r = rsqrtf(cta_sum(sum, part[0]) / p.H + p.eps);
-            if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[row] = r;
-        }
-#pragma unroll
-        for (int j = 0; j < ITERS; ++j) {
-            const int col = (j * blockDim.x + threadIdx.x) * VEC;
-            if (col >= p.H) continue;
-            float c[VEC];
+    for (int j = 0; j < ITERS; ++j) {
+        const int col = (j * blockDim.x + threadIdx.x) * VEC;
+        if (col >= p.H) continue;
+        rx[j].get(x[j]);
+        if (p.y) {
+            float n[VEC], c[VEC];
+            ry[j].get(n);
             if (p.w_post) {
-                load_param8(p.w_post, p.param_f32, col, c);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) n[j][i] *= r * c[i];
+                load_param(p.w_post, p.param_f32, col, c);
+                mul_vec(n, r_post);
+                mul_vec(n, c);
             }
             if (p.gate_kind != GATE_NONE) {
-                if (p.gate_kind == GATE_ROW) load_param8(p.gate, p.param_f32, col, c);
-                else load8(static_cast<const Y *>(p.gate) + at + col, c);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) n[j][i] *= c[i];
+                if (p.gate_kind == GATE_ROW) load_param(p.gate, p.param_f32, col, c);
+                else load_vec(static_cast<const Y *>(p.gate) + at + col, c);
+                mul_vec(n, c);
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j][i] = fmaf(p.alpha, n[j][i], x[j][i]);
-            store8(static_cast<X *>(p.x_out) + at + col, x[j]);
+            fma_vec(x[j], n, p.alpha);
+            store_vec(static_cast<X *>(p.x_out) + at + col, x[j]);
         }
+        dot_vec(sum, x[j], x[j]);
     }
     if (!p.w) return;
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < ITERS; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sum = fmaf(x[j][i], x[j][i], sum);
-    const float r = rsqrtf(cta_sum(sum, part[1]) / p.H + p.eps);
+    const float r = rsqrtf(fmaf(cta_sum(sum[0] + sum[1], part[1]), inv_h, p.eps));
     if (threadIdx.x == 0 && p.rstd) p.rstd[row] = r;
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
         const int col = (j * blockDim.x + threadIdx.x) * VEC;
-        const bool in = col < p.H;  // (the same in a block's 16 lanes where h is e4m3)
+        const bool in = col < p.H;  // (the same in a block's lanes where h is e4m3)
         float c[VEC] = {};
-        if (in) load_param8(p.w, p.param_f32, col, c);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) c[i] *= x[j][i] * r;
-        if (p.sf.sf) {
+        if (in) {
+            load_param(p.w, p.param_f32, col, c);
+            mul_vec(x[j], r);
+            mul_vec(c, x[j]);
+        }
+        if constexpr (FP8) {
             float scale;
-            const uint2 q = quantise8(c, block_amax(c), scale);
+            const uint2 q = quantise(c, block_amax(c), scale);
             if (in) {
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.h) + at + col) = q;
-                if ((threadIdx.x & 15) == 0) *p.sf.at(row, col >> 7) = scale;
+                if ((threadIdx.x & (BLOCK_LANES - 1)) == 0) p.sf.sf[static_cast<long long>(col >> 7) * p.sf.ld + row] = scale;
             }
         } else if (in) {
-            store8(static_cast<Y *>(p.h) + at + col, c);
+            store_vec(static_cast<Y *>(p.h) + at + col, c);
         }
     }
 }
 
-// CTA b takes rows b, b + CTAs, ...: the parameters' sums over its rows stay in registers and go to `partial` once.
+// Rows past NORM_RING_H columns, read from memory as they are needed.
 template <typename X, typename Y, int ITERS>
-__global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(const NormParams p) {
+__global__ void __launch_bounds__(NORM_WIDE_THREADS) rms_norm_backward_wide_kernel(const NormParams p) {
     __shared__ float part[2][32];
     grid_dependency_wait();
     grid_launch_dependents();
+    const float inv_h = 1.f / p.H;
     float sum_w[ITERS][VEC] = {}, sum_post[ITERS][VEC] = {}, sum_gate[ITERS][VEC] = {};
     for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
         const long long at = static_cast<long long>(row) * p.H;
         float dx[ITERS][VEC];
-#pragma unroll
-        for (int j = 0; j < ITERS; ++j) {
-            const int col = (j * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) dx[j][i] = 0.f;
-            if (p.d_x_out && col < p.H) load8(static_cast<const X *>(p.d_x_out) + at + col, dx[j]);
-        }
+        float r = 0.f, r_post = 1.f;
+        if (p.w) r = p.rstd[row];
+        if (p.w_post) r_post = p.rstd_post[row];
         if (p.w) {
-            const float r = *(p.rstd + row);
-            float x[ITERS][VEC], e[ITERS][VEC], sum = 0.f;
+            float x[ITERS][VEC], sum[2] = {};  // x r, and w d_h in dx
 #pragma unroll
             for (int j = 0; j < ITERS; ++j) {
                 const int col = (j * blockDim.x + threadIdx.x) * VEC;
-                float c[VEC] = {};
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) x[j][i] = e[j][i] = 0.f;
                 if (col < p.H) {
-                    load8(static_cast<const X *>(p.x) + at + col, x[j]);
-                    load8(static_cast<const Y *>(p.d_h) + at + col, e[j]);
-                    load_param8(p.w, p.param_f32, col, c);
-                }
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    x[j][i] *= r;
-                    sum_w[j][i] = fmaf(e[j][i], x[j][i], sum_w[j][i]);
-                    e[j][i] *= c[i];
-                    sum = fmaf(e[j][i], x[j][i], sum);
+                    float c[VEC];
+                    load_vec(static_cast<const X *>(p.x) + at + col, x[j]);
+                    load_vec(static_cast<const Y *>(p.d_h) + at + col, dx[j]);
+                    load_param(p.w, p.param_f32, col, c);
+                    mul_vec(x[j], r);
+                    fma_vec(sum_w[j], dx[j], x[j]);
+                    mul_vec(dx[j], c);
+                    dot_vec(sum, dx[j], x[j]);
                 }
             }
-            const float mean = cta_sum(sum, part[0]) / p.H;
+            const float mean = cta_sum(sum[0] + sum[1], part[0]) * inv_h;
 #pragma unroll
-            for (int j = 0; j < ITERS; ++j)
+            for (int j = 0; j < ITERS; ++j) {
+                const int col = (j * blockDim.x + threadIdx.x) * VEC;
+                if (col < p.H) {
+                    fma_vec(dx[j], x[j], -mean);
+                    if (p.d_x_out) {
+                        load_vec(static_cast<const X *>(p.d_x_out) + at + col, x[j]);
+                        fma_vec(x[j], dx[j], r);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) dx[j][i] = fmaf(r, e[j][i] - x[j][i] * mean, dx[j][i]);
-        }
-#pragma unroll
-        for (int j = 0; j < ITERS; ++j) {
-            const int col = (j * blockDim.x + threadIdx.x) * VEC;
-            if (col < p.H) store8(static_cast<X *>(p.d_x) + at + col, dx[j]);
-        }
-        if (!p.y) {
-            __syncthreads();  // part[0] is written again in the next row
-            continue;
-        }
-        const float r = p.w_post ? *(p.rstd_post + row) : 1.f;
-        float y[ITERS][VEC], sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < ITERS; ++j) {
-            const int col = (j * blockDim.x + threadIdx.x) * VEC;
-            float post[VEC], gate[VEC], d_gate[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) y[j][i] = 0.f, post[i] = gate[i] = 1.f;
-            if (col < p.H) {
-                load8(static_cast<const Y *>(p.y) + at + col, y[j]);
-                if (p.w_post) load_param8(p.w_post, p.param_f32, col, post);
-                if (p.gate_kind == GATE_ROW) load_param8(p.gate, p.param_f32, col, gate);
-                if (p.gate_kind == GATE_TOKEN) load8(static_cast<const Y *>(p.gate) + at + col, gate);
+                        for (int i = 0; i < VEC; ++i) dx[j][i] = x[j][i];
+                    } else {
+                        mul_vec(dx[j], r);
+                    }
+                }
             }
+        } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                y[j][i] *= r;
-                const float d = p.alpha * dx[j][i];
-                d_gate[i] = d * y[j][i] * post[i];
-                sum_gate[j][i] += d_gate[i];
-                const float dn = d * gate[i];
-                sum_post[j][i] = fmaf(dn, y[j][i], sum_post[j][i]);
-                dx[j][i] = dn * post[i];
-                sum = fmaf(dx[j][i], y[j][i], sum);
+            for (int j = 0; j < ITERS; ++j) {
+                const int col = (j * blockDim.x + threadIdx.x) * VEC;
+                if (col < p.H) load_vec(static_cast<const X *>(p.d_x_out) + at + col, dx[j]);
             }
-            if (p.gate_kind == GATE_TOKEN && col < p.H) store8(static_cast<Y *>(p.d_gate_token) + at + col, d_gate);
         }
-        float mean = 0.f;
-        if (p.w_post) mean = cta_sum(sum, part[1]) / p.H;
 #pragma unroll
         for (int j = 0; j < ITERS; ++j) {
             const int col = (j * blockDim.x + threadIdx.x) * VEC;
-            if (col >= p.H) continue;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) dx[j][i] = r * (dx[j][i] - y[j][i] * mean);
-            store8(static_cast<Y *>(p.d_y) + at + col, dx[j]);
+            if (col < p.H) store_vec(static_cast<X *>(p.d_x) + at + col, dx[j]);
         }
-        __syncthreads();
+        if (p.y) {
+            float n[ITERS][VEC], sum[2] = {};  // y r_post; from here on dx is the gradient of w_post n
+#pragma unroll
+            for (int j = 0; j < ITERS; ++j) {
+                const int col = (j * blockDim.x + threadIdx.x) * VEC;
+                if (col >= p.H) continue;
+                float c[VEC];
+                load_vec(static_cast<const Y *>(p.y) + at + col, n[j]);
+                mul_vec(n[j], r_post);
+                mul_vec(dx[j], p.alpha);
+                if (p.gate_kind != GATE_NONE) {  // d_gate = d n post, then d gate
+                    float d_gate[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) d_gate[i] = n[j][i];
+                    mul_vec(d_gate, dx[j]);
+                    if (p.w_post) {
+                        load_param(p.w_post, p.param_f32, col, c);
+                        mul_vec(d_gate, c);
+                    }
+                    if (p.gate_kind == GATE_ROW) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) sum_gate[j][i] += d_gate[i];
+                        load_param(p.gate, p.param_f32, col, c);
+                    } else {
+                        store_vec(static_cast<Y *>(p.d_gate_token) + at + col, d_gate);
+                        load_vec(static_cast<const Y *>(p.gate) + at + col, c);
+                    }
+                    mul_vec(dx[j], c);
+                }
+                if (p.w_post) {
+                    fma_vec(sum_post[j], dx[j], n[j]);
+                    load_param(p.w_post, p.param_f32, col, c);
+                    mul_vec(dx[j], c);
+                    dot_vec(sum, dx[j], n[j]);
+                }
+            }
+            const float mean = p.w_post ? cta_sum(sum[0] + sum[1], part[1]) * inv_h : 0.f;
+#pragma unroll
+            for (int j = 0; j < ITERS; ++j) {
+                const int col = (j * blockDim.x + threadIdx.x) * VEC;
+                if (col >= p.H) continue;
+                if (p.w_post) {
+                    fma_vec(dx[j], n[j], -mean);
+                    mul_vec(dx[j], r_post);
+                }
+                store_vec(static_cast<Y *>(p.d_y) + at + col, dx[j]);
+            }
+        }
+        if (!(p.w && p.w_post)) __syncthreads();
     }
     float *partial = p.partial + static_cast<long long>(blockIdx.x) * 3 * p.H;
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
         const int col = (j * blockDim.x + threadIdx.x) * VEC;
         if (col >= p.H) continue;
-        if (p.w) store8(partial + col, sum_w[j]);
-        if (p.w_post) store8(partial + p.H + col, sum_post[j]);
-        if (p.gate_kind == GATE_ROW) store8(partial + 2 * p.H + col, sum_gate[j]);
+        if (p.w) store_vec(partial + col, sum_w[j]);
+        if (p.w_post) store_vec(partial + p.H + col, sum_post[j]);
+        if (p.gate_kind == GATE_ROW) store_vec(partial + 2 * p.H + col, sum_gate[j]);
     }
 }
 
-constexpr int NORM_SUM_COLS = 64, NORM_SUM_PARTS = 16;
+constexpr int NORM_SUM_LANES = 16, NORM_SUM_PARTS = 64;  // lanes of four columns; parts of the CTAs
 
 // d[z][col] = sum over the CTAs' partial sums, in an order that does not change.  blockIdx.y: which of the three.
-__global__ void __launch_bounds__(NORM_SUM_COLS *NORM_SUM_PARTS)
+__global__ void __launch_bounds__(NORM_SUM_LANES *NORM_SUM_PARTS)
     rms_norm_sum_kernel(const float *partial, int ctas, int H, float *d0, float *d1, float *d2) {
-    __shared__ float part[NORM_SUM_PARTS][NORM_SUM_COLS];
+    __shared__ float4 part[NORM_SUM_PARTS][NORM_SUM_LANES];
     grid_dependency_wait();
     grid_launch_dependents();
     float *d = blockIdx.y == 0 ? d0 : blockIdx.y == 1 ? d1 : d2;
     if (!d) return;
-    const int col = blockIdx.x * NORM_SUM_COLS + threadIdx.x;
-    float sum = 0.f;
+    const int col = (blockIdx.x * NORM_SUM_LANES + threadIdx.x) * 4;  // (H is a multiple of 8)
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < H)
-        for (int b = threadIdx.y; b < ctas; b += NORM_SUM_PARTS)
-            sum += partial[(static_cast<long long>(b) * 3 + blockIdx.y) * H + col];
+#pragma unroll 4
+        for (int b = threadIdx.y; b < ctas; b += NORM_SUM_PARTS) {
+            const float4 v = *reinterpret_cast<const float4 *>(partial + (static_cast<long long>(b) * 3 + blockIdx.y) * H + col);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
     part[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
-    if (threadIdx.y == 0 && col < H) {
-        sum = 0.f;
-        for (int i = 0; i < NORM_SUM_PARTS; ++i) sum += part[i][threadIdx.x];
-        d[col] = sum;
+    const int t = threadIdx.y * NORM_SUM_LANES + threadIdx.x;  // a thread a column
+    const int out = blockIdx.x * NORM_SUM_LANES * 4 + t;
+    if (t < NORM_SUM_LANES * 4 && out < H) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < NORM_SUM_PARTS; ++i) s += reinterpret_cast<const float *>(part[i])[t];
+        d[out] = s;
     }
 }
 

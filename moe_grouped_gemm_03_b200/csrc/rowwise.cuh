@@ -11,8 +11,8 @@
 namespace dg {
 
 using bf16 = __nv_bfloat16;
-constexpr int VEC = 8;                         // elements a lane handles at a time: 16 bytes of bf16
-constexpr int BLOCK_LANES = 128 / VEC;         // lanes that hold one block of 128 (half a warp)
+constexpr int VEC = 8;  // elements a lane handles at a time: 16 bytes of bf16
+constexpr int BLOCK_LANES = 128 / VEC;  // lanes that hold one block of 128 (half a warp)
 constexpr unsigned ERR_WORD_BAD_GROUP = 2u;    // device error word of DG_ERR_BAD_GROUP
 
 __device__ __forceinline__ void raise_bad_group(unsigned *err) { atomicCAS(err, 0u, ERR_WORD_BAD_GROUP); }
@@ -27,15 +27,41 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// (stream: a load of what is read once and need not stay in L1.)
+
+// Asynchronous copies of 16 bytes to shared memory, past L1, waited for in groups by the thread that made them.
+__device__ __forceinline__ void copy_async16(void *s, const void *p) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s)), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_async_wait() {  // until at most N groups are under way
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Loads are ordinary ones, not the non-coherent kind (__ldg): a kernel here may start before the one that writes its
 // inputs has ended, and memory that changes during a kernel's life is not for that path.
 
-// One lane's vector of eight elements as it lies in memory (bf16: 16 bytes, fp32: 32 bytes, each at a multiple of that).
-template <typename T> struct Raw8;
-template <> struct Raw8<bf16> {
+// One lane's vector of eight elements as it lies in memory, at a multiple of its size (at most 32 bytes).  Loads and stores of
+// 32 bytes are single 256-bit accesses: as two of 128 bits, half of each request's sectors went unused.
+__device__ __forceinline__ void load256(uint32_t (&w)[8], const void *p) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store256(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <typename T> struct Raw;
+template <> struct Raw<bf16> {
     uint4 a;
     __device__ __forceinline__ void load(const bf16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
+    static constexpr int UNITS = 1;  // 16-byte units of a vector in shared memory, `plane` units apart
+    static __device__ __forceinline__ void load_async(uint4 *s, int, const bf16 *p) { copy_async16(s, p); }
+    __device__ __forceinline__ void load_shared(const uint4 *s, int) { a = *s; }
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
         unpack_bf16x2(a.x, v[0], v[1]);
         unpack_bf16x2(a.y, v[2], v[3]);
@@ -47,37 +73,80 @@ template <> struct Raw8<bf16> {
                        pack_bf16x2(v[6], v[7]));
     }
 };
-template <> struct Raw8<float> {  // one 256-bit access: as two of 128 bits, half of each request's sectors went unused
-    float v8[VEC];
-    __device__ __forceinline__ void load(const float *p) {
-        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=f"(v8[0]), "=f"(v8[1]), "=f"(v8[2]), "=f"(v8[3]), "=f"(v8[4]), "=f"(v8[5]), "=f"(v8[6]), "=f"(v8[7])
-                     : "l"(p));
+template <> struct Raw<float> {
+    uint32_t w[VEC];
+    __device__ __forceinline__ void load(const float *p) { load256(w, p); }
+    __device__ __forceinline__ void store(float *p) const { store256(p, w); }
+    static constexpr int UNITS = 2;
+    static __device__ __forceinline__ void load_async(uint4 *s, int plane, const float *p) {
+        copy_async16(s, p);
+        copy_async16(s + plane, p + 4);
     }
-    __device__ __forceinline__ void store(float *p) const {
-        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v8[0]), "f"(v8[1]), "f"(v8[2]),
-                     "f"(v8[3]), "f"(v8[4]), "f"(v8[5]), "f"(v8[6]), "f"(v8[7])
-                     : "memory");
+    __device__ __forceinline__ void load_shared(const uint4 *s, int plane) {
+        const uint4 a = s[0], b = s[plane];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
     }
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = v8[i];
+        for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(w[i]);
     }
     __device__ __forceinline__ void set(const float (&v)[VEC]) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v8[i] = v[i];
+        for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(v[i]);
     }
 };
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[VEC]) {
-    Raw8<T> r;
+template <typename T> __device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
+    Raw<T> r;
     r.load(p);
     r.get(v);
 }
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[VEC]) {
-    Raw8<T> r;
+template <typename T> __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
+    Raw<T> r;
     r.set(v);
     r.store(p);
+}
+
+// Two fp32 operations an instruction, on the pairs of a vector (the kernels here run out of issue slots before they run out
+// of arithmetic): a *= b, a *= s, a += b * c, a = a * s + b.
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
+    asm("{.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float &c0, float &c1, float a0, float a1, float b0, float b1) {  // c += a * b
+    asm("{.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;}"
+        : "+f"(c0), "+f"(c1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul_vec(float (&a)[VEC], const float (&b)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) mul2(a[i], a[i + 1], b[i], b[i + 1]);
+}
+__device__ __forceinline__ void mul_vec(float (&a)[VEC], float s) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) mul2(a[i], a[i + 1], s, s);
+}
+__device__ __forceinline__ void fma_vec(float (&c)[VEC], const float (&a)[VEC], const float (&b)[VEC]) {  // c += a * b
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) fma2(c[i], c[i + 1], a[i], a[i + 1], b[i], b[i + 1]);
+}
+__device__ __forceinline__ void fma_vec(float (&c)[VEC], const float (&a)[VEC], float s) {  // c += a * s
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) fma2(c[i], c[i + 1], a[i], a[i + 1], s, s);
+}
+// Sum of products of a vector, onto a pair of partial sums.
+__device__ __forceinline__ void dot_vec(float (&sum)[2], const float (&a)[VEC], const float (&b)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) fma2(sum[0], sum[1], a[i], a[i + 1], b[i], b[i + 1]);
+}
+
+__device__ __forceinline__ float absmax3(float a, float b, float c) {  // NaN is passed over
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {  // a in the lowest byte
@@ -91,19 +160,19 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 __device__ __forceinline__ float block_amax(const float (&v)[VEC]) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < VEC; i += 2) m = absmax3(m, v[i], v[i + 1]);
     const unsigned lanes = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
     for (int d = BLOCK_LANES / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
     return m;
 }
 
-// Quantises one lane's eight values of a block whose largest |v| is `amax` (the same in the block's 16 lanes, which
-// all call this).  scale = 2^ceil(log2(amax / 448)), the smallest power of two that brings every value within e4m3's
-// +-448 (at least 2^-126; 1 for a block of zeros); codes = e4m3 RNE(v / scale), where the division is an exact
-// multiplication by the inverse power.  A value that is not finite gets e4m3's NaN code, and the scale goes by the
-// block's finite values, so that it does not flatten its neighbours.
-__device__ __forceinline__ uint2 quantise8(float (&v)[VEC], float amax, float &scale) {
+// Quantises one lane's values of a block whose largest |v| is `amax` (the same in the block's lanes, which all call this).
+// scale = 2^ceil(log2(amax / 448)), the smallest power of two that brings every value within e4m3's +-448 (at least
+// 2^-126; 1 for a block of zeros); codes = e4m3 RNE(v / scale), where the division is an exact multiplication by the
+// inverse power.  A value that is not finite gets e4m3's NaN code, and the scale goes by the block's finite values, so that
+// it does not flatten its neighbours.
+__device__ __forceinline__ uint2 quantise(float (&v)[VEC], float amax, float &scale) {
     if (__builtin_expect(!(amax < __int_as_float(0x7f800000)), 0)) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
@@ -115,9 +184,8 @@ __device__ __forceinline__ uint2 quantise8(float (&v)[VEC], float amax, float &s
     int e = static_cast<int>((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;
     e = amax == 0.f ? 127 : max(e, 1);
     scale = __uint_as_float(static_cast<uint32_t>(e) << 23);
-    const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // (e <= 247)
-    return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                      e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+    mul_vec(v, __uint_as_float(static_cast<uint32_t>(254 - e) << 23));  // (e <= 247)
+    return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
 }
 
 // Scales of an e4m3 operand, MN-major: [groups][cols / 128][ld], rows_per_group rows in each group.
