@@ -61,28 +61,55 @@ __device__ __forceinline__ float cta_sum(float v, float *part) {
     return v;
 }
 
-// A thread's vectors in shared memory: the parameters (w, w_post, a gate [H]) and the stages of a row's tensors, each vector
-// of T as Raw<T>::UNITS units of 16 bytes, a unit of all threads side by side.
+// A thread's vectors in shared memory: the parameters (w, w_post, a gate [H]) and the stages of a row's tensors, in planes of
+// one 16-byte unit a thread; a bf16 vector is a unit, an fp32 vector two.  A thread copies what it will read itself, but for
+// the rows in fp32: copies are 16 bytes a lane, and so that the lanes of a warp copy runs of memory its 64 units are copied
+// in memory order, 32 to a plane (in an order that lets eight lanes reading every other unit meet eight banks; each lane
+// copying its own two units took 159 us where this takes 110).
 struct NormSlots {
     uint4 *mine;
     int stage;  // first unit of the stage in use
 
     __device__ __forceinline__ uint4 *unit(int n) const { return mine + n * static_cast<int>(blockDim.x); }
-    template <typename T> __device__ __forceinline__ void copy(int n, const void *src, long long i) const {
-        Raw<T>::load_async(unit(n), blockDim.x, static_cast<const T *>(src) + i);
+    static __device__ __forceinline__ int turned(int unit) { return unit ^ (unit >> 3 & 1); }
+
+    // the vector at `src`, columns col .. col + 7 (of `width`) of a row; `in`: whether they exist
+    __device__ __forceinline__ void copy(int n, const bf16 *src, int, int, bool in) const {
+        if (in) copy_async16(unit(n), src);
+    }
+    __device__ __forceinline__ void copy(int n, const float *src, int col, int width, bool) const {
+        const int lane = threadIdx.x & 31, c = col - 4 * lane, place = turned(lane) - lane;
+        if (c < width) copy_async16(unit(n) + place, src - 4 * lane);
+        if (c + 128 < width) copy_async16(unit(n + 1) + place, src - 4 * lane + 128);
+    }
+    __device__ __forceinline__ void get(int n, const bf16 *, float (&v)[VEC]) const {
+        Raw<bf16> raw;
+        raw.a = *unit(n);
+        raw.get(v);
+    }
+    __device__ __forceinline__ void get(int n, const float *, float (&v)[VEC]) const {
+        const int lane = threadIdx.x & 31, first = 2 * lane & 31;
+        const uint4 *s = unit(n + (lane >> 4)) - lane;
+        halves(s[turned(first)], s[turned(first + 1)], v);
     }
     template <typename T> __device__ __forceinline__ void get(int n, float (&v)[VEC]) const {
-        Raw<T> raw;
-        raw.load_shared(unit(n), blockDim.x);
-        raw.get(v);
+        get(n, static_cast<const T *>(nullptr), v);
+    }
+    static __device__ __forceinline__ void halves(uint4 a, uint4 b, float (&v)[VEC]) {
+        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
     }
     // parameter number i
     __device__ __forceinline__ void copy_param(int i, const void *src, int f32, int col) const {
-        if (f32) copy<float>(2 * i, src, col);
-        else copy<bf16>(i, src, col);
+        if (f32) {
+            copy_async16(unit(2 * i), static_cast<const float *>(src) + col);
+            copy_async16(unit(2 * i + 1), static_cast<const float *>(src) + col + 4);
+        } else {
+            copy_async16(unit(i), static_cast<const bf16 *>(src) + col);
+        }
     }
     __device__ __forceinline__ void get_param(int i, int f32, float (&v)[VEC]) const {
-        if (f32) get<float>(2 * i, v);
+        if (f32) halves(*unit(2 * i), *unit(2 * i + 1), v);
         else get<bf16>(i, v);
     }
 };
@@ -121,25 +148,27 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
     grid_dependency_wait();
     grid_launch_dependents();
     auto fill = [&](long long row, int stage) {
-        if (in && row < p.T) {
+        if (row < p.T && (UX > 1 || in)) {  // (in fp32 a lane copies other columns than its own)
             const long long at = row * p.H + col;
             if (has_w) {
-                s.copy<X>(stage + UX, p.x, at);
-                s.copy<Y>(stage + 2 * UX, p.d_h, at);
+                s.copy(stage + UX, static_cast<const X *>(p.x) + at, col, p.H, UX == 1 || in);
+                s.copy(stage + 2 * UX, static_cast<const Y *>(p.d_h) + at, col, p.H, UX == 1 || in);
             }
-            if (p.d_x_out) s.copy<X>(stage, p.d_x_out, at);
-            if (has_y) s.copy<Y>(stage + y_unit, p.y, at);
-            if (GATE == GATE_TOKEN) s.copy<Y>(stage + y_unit + UY, p.gate, at);
+            if (p.d_x_out) s.copy(stage, static_cast<const X *>(p.d_x_out) + at, col, p.H, UX == 1 || in);
+            if (has_y) s.copy(stage + y_unit, static_cast<const Y *>(p.y) + at, col, p.H, UX == 1 || in);
+            if (GATE == GATE_TOKEN) s.copy(stage + y_unit + UY, static_cast<const Y *>(p.gate) + at, col, p.H, UX == 1 || in);
         }
-        copy_async_commit();
+        copy_async_commit();  // (a group for every stage, empty past the last row: the waits count them)
     };
-    if (in) {
+    if (in) {  // (with the first stage's group)
         if (has_w) s.copy_param(0, p.w, p.param_f32, col);
         if (p.w_post) s.copy_param(1, p.w_post, p.param_f32, col);
         if (GATE == GATE_ROW) s.copy_param(2, p.gate, p.param_f32, col);
     }
     for (int i = 0; i < p.stages; ++i) fill(blockIdx.x + static_cast<long long>(i) * gridDim.x, first_stage + i * stage_units);
-    float sum_w[VEC] = {}, sum_post[VEC] = {}, sum_gate[VEC] = {};
+    // sum_n: of alpha d_x y r_post, times w_post the gradient of a gate [H] and times that gate the one of w_post; of alpha
+    // d_x gate y r_post with a gate [T][H]
+    float sum_w[VEC] = {}, sum_n[VEC] = {};
     float r = 0.f, r_post = 1.f;  // of the row to come, loaded a row ahead
     if (has_w) r = p.rstd[blockIdx.x];
     if (p.w_post) r_post = p.rstd_post[blockIdx.x];
@@ -150,6 +179,7 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
         if (has_w) r_next = p.rstd[next];
         if (p.w_post) r_post_next = p.rstd_post[next];
         wait_stage(p.stages);
+        if (UX > 1) __syncwarp();  // fp32 rows are copied by other lanes
         float dx[VEC] = {}, t[VEC] = {}, c[VEC] = {};
         if (has_w) {
             float sum[2] = {};
@@ -182,7 +212,7 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
                 s.get<Y>(s.stage + y_unit, t);
                 mul_vec(t, r_post);
                 mul_vec(dx, p.alpha);
-                if (GATE != GATE_NONE) {  // d_gate = alpha d_x n, n = t w_post
+                if (GATE == GATE_TOKEN) {  // d_gate = alpha d_x n, n = t w_post
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) c[i] = t[i];
                     mul_vec(c, dx);
@@ -191,18 +221,16 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
                         s.get_param(1, p.param_f32, post);
                         mul_vec(c, post);
                     }
-                    if (GATE == GATE_ROW) {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) sum_gate[i] += c[i];
-                        s.get_param(2, p.param_f32, c);
-                    } else {
-                        store_vec(static_cast<Y *>(p.d_gate_token) + at, c);
-                        s.get<Y>(s.stage + y_unit + UY, c);
-                    }
+                    store_vec(static_cast<Y *>(p.d_gate_token) + at, c);
+                    s.get<Y>(s.stage + y_unit + UY, c);
+                    mul_vec(dx, c);
+                }
+                fma_vec(sum_n, dx, t);
+                if (GATE == GATE_ROW) {
+                    s.get_param(2, p.param_f32, c);
                     mul_vec(dx, c);
                 }
                 if (p.w_post) {
-                    fma_vec(sum_post, dx, t);
                     s.get_param(1, p.param_f32, c);
                     mul_vec(dx, c);
                     dot_vec(sum, dx, t);
@@ -215,6 +243,7 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
             }
             if (in) store_vec(static_cast<Y *>(p.d_y) + at, dx);
         }
+        if (UX > 1) __syncwarp();  // every lane has read the stage
         fill(row + static_cast<long long>(p.stages) * gridDim.x, s.stage);
         s.stage += stage_units;
         if (s.stage == first_stage + p.stages * stage_units) s.stage = first_stage;
@@ -225,8 +254,23 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
     if (!in) return;
     float *partial = p.partial + static_cast<long long>(blockIdx.x) * 3 * p.H + col;
     if (has_w) store_vec(partial, sum_w);
-    if (p.w_post) store_vec(partial + p.H, sum_post);
-    if (GATE == GATE_ROW) store_vec(partial + 2 * p.H, sum_gate);
+    float c[VEC];
+    if (p.w_post) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum_w[i] = sum_n[i];
+        if (GATE == GATE_ROW) {
+            s.get_param(2, p.param_f32, c);
+            mul_vec(sum_w, c);
+        }
+        store_vec(partial + p.H, sum_w);
+    }
+    if (GATE == GATE_ROW) {
+        if (p.w_post) {
+            s.get_param(1, p.param_f32, c);
+            mul_vec(sum_n, c);
+        }
+        store_vec(partial + 2 * p.H, sum_n);
+    }
 }
 
 // One CTA a row, which waits for the sums in registers; ITERS vectors a thread.

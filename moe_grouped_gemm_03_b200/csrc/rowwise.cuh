@@ -59,9 +59,7 @@ template <> struct Raw<bf16> {
     uint4 a;
     __device__ __forceinline__ void load(const bf16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = a; }
-    static constexpr int UNITS = 1;  // 16-byte units of a vector in shared memory, `plane` units apart
-    static __device__ __forceinline__ void load_async(uint4 *s, int, const bf16 *p) { copy_async16(s, p); }
-    __device__ __forceinline__ void load_shared(const uint4 *s, int) { a = *s; }
+    static constexpr int UNITS = 1;  // of 16 bytes
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
         unpack_bf16x2(a.x, v[0], v[1]);
         unpack_bf16x2(a.y, v[2], v[3]);
@@ -78,14 +76,6 @@ template <> struct Raw<float> {
     __device__ __forceinline__ void load(const float *p) { load256(w, p); }
     __device__ __forceinline__ void store(float *p) const { store256(p, w); }
     static constexpr int UNITS = 2;
-    static __device__ __forceinline__ void load_async(uint4 *s, int plane, const float *p) {
-        copy_async16(s, p);
-        copy_async16(s + plane, p + 4);
-    }
-    __device__ __forceinline__ void load_shared(const uint4 *s, int plane) {
-        const uint4 a = s[0], b = s[plane];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    }
     __device__ __forceinline__ void get(float (&v)[VEC]) const {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = __uint_as_float(w[i]);
