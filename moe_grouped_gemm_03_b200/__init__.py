@@ -41,6 +41,11 @@ if not os.path.exists(LIB_PATH):
                       "(or __graft_entry__.build()); there is no non-CUDA implementation")
 
 _lib = ctypes.CDLL(LIB_PATH)
+if not os.path.exists(os.path.join(_HERE, "_rowwise.so")):
+    raise ImportError(f"{os.path.join(_HERE, '_rowwise.so')} is missing: build it with __graft_entry__.build()")
+from . import _rowwise  # noqa: E402  (the binding of the row-wise operators, linked to libdg.so)
+
+_rowwise.set_error(DGError)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _LL = ctypes.c_longlong
@@ -432,76 +437,8 @@ def m_grouped_fp8_gemm_nt_nopad(lhs, rhs, out: torch.Tensor, counts: torch.Tenso
 
 
 # --------------------------------------------------------------------------- dispatch, combine, SwiGLU and norms
-_ACT_TYPES = (torch.bfloat16, torch.float32)
-_TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}  # dg_dtype
-_ID_TYPES = (torch.int32, torch.int64)
-_F32, _I32 = (torch.float32,), (torch.int32,)
-
-
-def _check_tensors(*named) -> None:
-    """(name, tensor, shape, dtypes) of the arguments of a row-wise call: contiguous CUDA tensors, all on the current
-    device, on whose current stream the call runs.  The passing path is a handful of attribute look-ups and formats no
-    message: these calls last a few microseconds."""
-    device = torch._C._cuda_getDevice()
-    for name, t, shape, dtypes in named:
-        try:
-            if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device:
-                continue
-        except AttributeError:
-            pass
-        _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
-        _need(t.dtype in dtypes, f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-        _need(t.shape == shape, f"{name} must be {list(shape)}, got {list(t.shape)}")
-        _need(t.is_contiguous(), f"{name} must be contiguous")
-        _need(t.is_cuda, f"{name} must be a CUDA tensor")
-        _need(False, f"{name} is on device {t.get_device()}, the current one is {device}")
-
-
-def _check_optional(*named) -> None:
-    """The same for arguments that may be None."""
-    _check_tensors(*[n for n in named if n[1] is not None])
-
-
-def _raw_stream() -> int:
-    """The current stream of the current device, without building a Stream object."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-
-
-def _dims(name, t, least, most=None):
-    """Shape of a tensor argument that has `least` (or up to `most`) dimensions."""
-    try:
-        shape = t.shape
-        if least <= len(shape) <= (most or least):
-            return shape
-    except AttributeError:
-        pass
-    _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
-    raise DGError(-1, f"{name} must have {least if most is None else f'{least} or {most}'} dims, got {tuple(t.shape)}")
-
-
-def _row_operand(name, out, cols, dtype):
-    """A row operand, [rows, cols] or [G, M_max, cols]: a tensor of `dtype`, or (e4m3 codes, sf) as a GEMM's lhs.
-    Returns (codes or tensor, sf or None, rows, rows_per_group)."""
-    if isinstance(out, (tuple, list)):
-        if not (len(out) == 2):
-            raise DGError(-1, f"{name} must be a tensor or a pair (codes, scales)")
-        a, sf = out
-        shape = _dims(name, a, 2, 3)
-        if not (isinstance(sf, torch.Tensor)):
-            raise DGError(-1, f"{name} scales must be a torch.Tensor")
-        per = shape[-2]
-        groups = shape[:-2]
-        _check_tensors((name, a, (*groups, per, cols), _FP8_TYPES),
-                       (name + " scales", sf, (*groups, cols // 128, (per + 3) // 4 * 4), _F32))
-    else:
-        a, sf = out, None
-        shape = _dims(name, a, 2, 3)
-        per = shape[-2]
-        groups = shape[:-2]
-        _check_tensors((name, a, (*groups, per, cols), (dtype,)))
-    return a, sf, per * groups[0] if groups else per, per
-
-
+# Checked and called in _rowwise (csrc/rowwise_binding.cpp): contiguous CUDA tensors on the current device, on whose current
+# stream the calls run; DGError for anything else.
 def get_m_total_bound(num_slots: int, num_groups: int) -> int:
     """Rows the contiguous layout needs at most for num_slots routed slots and num_groups groups (the size of m_indices,
     and of the GEMM's operands, when the counts are known on the device only)."""
@@ -510,102 +447,45 @@ def get_m_total_bound(num_slots: int, num_groups: int) -> int:
     return n
 
 
-def _sort_args(topk_ids, row_of_slot, counts):
-    T, k = _dims("topk_ids", topk_ids, 2)
-    G, = _dims("counts", counts, 1)
-    _check_tensors(("topk_ids", topk_ids, (T, k), _ID_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32),
-                   ("counts", counts, (G,), _I32))
-    return _ptr(topk_ids), topk_ids.element_size(), T, k, G
-
-
 def moe_sort_contiguous(topk_ids: torch.Tensor, row_of_slot: torch.Tensor, m_indices: torch.Tensor,
                         counts: torch.Tensor) -> None:
     """Rows of the routed slots in the contiguous layout.  topk_ids [T, k] (int32 or int64; -1: no row) -> row_of_slot
     int32 [T, k] (-1: none), m_indices int32 [M_total] as m_grouped_fp8_gemm_nt_contiguous takes it (M_total:
     get_m_total_bound, or any multiple of the alignment that has room), counts int32 [G] rows of each group."""
-    args = _sort_args(topk_ids, row_of_slot, counts)
-    M, = _dims("m_indices", m_indices, 1)
-    _check_tensors(("m_indices", m_indices, (M,), _I32))
-    _check(_lib.dg_moe_sort_contiguous(*args, M, _ptr(row_of_slot), _ptr(m_indices), _ptr(counts), _raw_stream()))
+    _rowwise.moe_sort_contiguous(topk_ids, row_of_slot, m_indices, counts)
 
 
 def moe_sort_nopad(topk_ids: torch.Tensor, row_of_slot: torch.Tensor, counts: torch.Tensor) -> None:
     """Rows of the routed slots in the no-padding layout: row_of_slot int32 [T, k], counts int32 [G] as
     m_grouped_fp8_gemm_nt_nopad takes them."""
-    args = _sort_args(topk_ids, row_of_slot, counts)
-    _check(_lib.dg_moe_sort_nopad(*args, _ptr(row_of_slot), _ptr(counts), _raw_stream()))
+    _rowwise.moe_sort_nopad(topk_ids, row_of_slot, counts)
 
 
 def moe_sort_masked(topk_ids: torch.Tensor, row_of_slot: torch.Tensor, masked_m: torch.Tensor, m_max: int) -> None:
     """Rows of the routed slots in the masked layout (row g * m_max + i): row_of_slot int32 [T, k], masked_m int32 [G] as
     m_grouped_fp8_gemm_nt_masked takes it.  Slots past m_max of their group get no row (DG_ERR_BAD_GROUP)."""
-    args = _sort_args(topk_ids, row_of_slot, masked_m)
-    _check(_lib.dg_moe_sort_masked(*args, int(m_max), _ptr(row_of_slot), _ptr(masked_m), _raw_stream()))
+    _rowwise.moe_sort_masked(topk_ids, row_of_slot, masked_m, m_max)
 
 
 def moe_permute(x: torch.Tensor, row_of_slot: torch.Tensor, out) -> None:
     """Dispatch: out[row_of_slot[t, s]] = x[t].  x [T, H] bf16 or fp32; out [rows, H] or [G, M_max, H] of x's type, or the
     pair (e4m3, sfa) that a grouped GEMM takes as lhs.  Rows without a slot are left as they were.  The gradient of x is
     moe_unpermute of the rows' gradient without weights."""
-    T, H = _dims("x", x, 2)
-    _, k = _dims("row_of_slot", row_of_slot, 2)
-    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32))
-    a, sf, rows, per = _row_operand("out", out, H, x.dtype)
-    _check(_lib.dg_moe_permute(_ptr(x), _TYPE_CODES[x.dtype], _ptr(row_of_slot), T, k, H, rows, per, _ptr(a), _ptr(sf),
-                               _raw_stream()))
+    _rowwise.moe_permute(x, row_of_slot, out)
 
 
 def moe_unpermute(rows: torch.Tensor, row_of_slot: torch.Tensor, out: torch.Tensor,
                   weights: Optional[torch.Tensor] = None) -> None:
     """Combine: out[t] = sum_s weights[t, s] * rows[row_of_slot[t, s]] over the slots with a row, summed in fp32 in the
     slots' order.  rows [R, H] or [G, M_max, H], out [T, H] of the same type; weights fp32 [T, k], None for 1."""
-    shape = _dims("rows", rows, 2, 3)
-    H, R = shape[-1], shape[-2] * (shape[0] if len(shape) == 3 else 1)
-    T, k = _dims("row_of_slot", row_of_slot, 2)
-    _check_tensors(("rows", rows, shape, _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32),
-                   ("out", out, (T, H), (rows.dtype,)))
-    if weights is not None:
-        _check_tensors(("weights", weights, (T, k), _F32))
-    _check(_lib.dg_moe_unpermute(_ptr(rows), _TYPE_CODES[rows.dtype], _ptr(row_of_slot), _ptr(weights), T, k, H, R,
-                                 _ptr(out), _raw_stream()))
+    _rowwise.moe_unpermute(rows, row_of_slot, out, weights)
 
 
 def moe_unpermute_backward(d_out: torch.Tensor, rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor,
                            d_rows, d_weights: torch.Tensor) -> None:
     """Gradient of moe_unpermute: d_rows[row_of_slot[t, s]] = weights[t, s] * d_out[t] (shaped as rows and of their type,
     or the pair (e4m3, sf)), d_weights[t, s] = <d_out[t], rows[row_of_slot[t, s]]> fp32 (0 for a slot without a row)."""
-    shape = _dims("rows", rows, 2, 3)
-    H = shape[-1]
-    T, k = _dims("row_of_slot", row_of_slot, 2)
-    _check_tensors(("rows", rows, shape, _ACT_TYPES), ("row_of_slot", row_of_slot, (T, k), _I32),
-                   ("d_out", d_out, (T, H), (rows.dtype,)), ("weights", weights, (T, k), _F32),
-                   ("d_weights", d_weights, (T, k), _F32))
-    a, sf, R, per = _row_operand("d_rows", d_rows, H, rows.dtype)
-    if not (a.shape == shape):
-        raise DGError(-1, f"d_rows must be shaped as rows, {list(shape)}, got {list(a.shape)}")
-    _check(_lib.dg_moe_unpermute_backward(_ptr(d_out), _ptr(rows), _TYPE_CODES[rows.dtype], _ptr(row_of_slot),
-                                          _ptr(weights), T, k, H, R, per, _ptr(a), _ptr(sf), _ptr(d_weights), _raw_stream()))
-
-
-def _swiglu_args(gate_up, out, out_name, out_cols, m_indices, counts, masked_m):
-    shape = gate_up.shape
-    a, sf, R, per = _row_operand(out_name, out, out_cols, gate_up.dtype)
-    if not (a.shape[:-1] == shape[:-1]):
-        raise DGError(-1, f"{out_name} must have the rows of gate_up, {list(shape[:-1])}")
-    _need((m_indices is not None) + (counts is not None) + (masked_m is not None) <= 1,
-          "at most one of m_indices, counts and masked_m may be given")
-    G = 0
-    if m_indices is not None:
-        _check_tensors(("m_indices", m_indices, (R,), _I32))
-    elif counts is not None:
-        G, = _dims("counts", counts, 1)
-        _check_tensors(("counts", counts, (G,), _I32))
-    elif masked_m is not None:
-        G, = _dims("masked_m", masked_m, 1)
-        _check_tensors(("masked_m", masked_m, (G,), _I32))
-    _need((len(shape) == 3) == (masked_m is not None) and (masked_m is None or G == shape[0]),
-          "tensors of three dims [G, M_max, ...] go with masked_m [G], and masked_m with them")
-    return a, sf, R, G
+    _rowwise.moe_unpermute_backward(d_out, rows, row_of_slot, weights, d_rows, d_weights)
 
 
 def swiglu(gate_up: torch.Tensor, out, m_indices: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
@@ -613,71 +493,30 @@ def swiglu(gate_up: torch.Tensor, out, m_indices: Optional[torch.Tensor] = None,
     """out = silu(g) * u on the rows that the groups own, gate_up [R, 2 I] = [g | u] (masked: [G, M_max, 2 I]); out [R, I]
     of the same type, or the pair (e4m3, sfa) that the next grouped GEMM takes as lhs.  m_indices, counts or masked_m as
     the GEMM that wrote gate_up took it; none: every row.  Other rows are left as they were."""
-    shape = _dims("gate_up", gate_up, 2, 3)
-    _need(shape[-1] % 2 == 0, "gate_up must have an even number of columns")
-    I = shape[-1] // 2
-    _check_tensors(("gate_up", gate_up, shape, _ACT_TYPES))
-    a, sf, R, G = _swiglu_args(gate_up, out, "out", I, m_indices, counts, masked_m)
-    _check(_lib.dg_swiglu(_ptr(gate_up), _TYPE_CODES[gate_up.dtype], R, I, _ptr(m_indices), _ptr(counts), _ptr(masked_m),
-                          G, _ptr(a), _ptr(sf), _raw_stream()))
+    _rowwise.swiglu(None, gate_up, out, m_indices, counts, masked_m)
 
 
 def swiglu_backward(d_out: torch.Tensor, gate_up: torch.Tensor, d_gate_up, m_indices: Optional[torch.Tensor] = None,
                     counts: Optional[torch.Tensor] = None, masked_m: Optional[torch.Tensor] = None) -> None:
     """Gradient of swiglu: d_gate_up [R, 2 I] = [d_g | d_u] (gate_up's type, or the pair (e4m3, sf) for the data-gradient
     GEMM) from d_out [R, I] and the forward's gate_up, on the same rows."""
-    shape = _dims("gate_up", gate_up, 2, 3)
-    _need(shape[-1] % 2 == 0, "gate_up must have an even number of columns")
-    I = shape[-1] // 2
-    _check_tensors(("gate_up", gate_up, shape, _ACT_TYPES), ("d_out", d_out, (*shape[:-1], I), (gate_up.dtype,)))
-    a, sf, R, G = _swiglu_args(gate_up, d_gate_up, "d_gate_up", 2 * I, m_indices, counts, masked_m)
-    _check(_lib.dg_swiglu_backward(_ptr(d_out), _ptr(gate_up), _TYPE_CODES[gate_up.dtype], R, I, _ptr(m_indices),
-                                   _ptr(counts), _ptr(masked_m), G, _ptr(a), _ptr(sf), _raw_stream()))
+    if d_out is None:
+        raise DGError(-1, "d_out must be a torch.Tensor")
+    _rowwise.swiglu(d_out, gate_up, d_gate_up, m_indices, counts, masked_m)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, out, eps: float = 1e-6, rstd: Optional[torch.Tensor] = None) -> None:
     """out = x * r * weight, r = 1 / sqrt(mean(x^2) + eps) in each row.  x [T, H] bf16 or fp32; weight [H] bf16 or fp32;
     out [T, H] bf16 (fp32 with an fp32 x), or the pair (e4m3, sfa) that fp8_gemm_nt takes as lhs.  rstd fp32 [T] keeps r
     for rms_norm_backward."""
-    T, H = _dims("x", x, 2)
-    pair = isinstance(out, (tuple, list))
-    out_type = torch.bfloat16 if pair else getattr(out, "dtype", None)
-    _need(out_type in _ACT_TYPES, "out must be bf16 or fp32, or a pair (e4m3, sfa)")
-    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("weight", weight, (H,), _ACT_TYPES))
-    if rstd is not None:
-        _check_tensors(("rstd", rstd, (T,), _F32))
-    a, sf, R, _ = _row_operand("out", out, H, out_type)
-    if not (tuple(a.shape) == (T, H)):
-        raise DGError(-1, f"out must be {[T, H]}, got {list(a.shape)}")
-    _check(_lib.dg_rms_norm(_ptr(x), _TYPE_CODES[x.dtype], _ptr(weight), _TYPE_CODES[weight.dtype], eps, T, H, _ptr(a),
-                            _TYPE_CODES[out_type], _ptr(sf), _ptr(rstd), _raw_stream()))
+    _rowwise.rms_norm(x, weight, out, eps, rstd)
 
 
 def rms_norm_backward(d_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, d_x: torch.Tensor,
                       d_weight: torch.Tensor, d_skip: Optional[torch.Tensor] = None) -> None:
     """Gradient of rms_norm: d_x [T, H] of x's type, plus d_skip (the gradient that reaches x past the norm; may be d_x
     itself), and d_weight fp32 [H].  d_out [T, H] of the forward's output type before quantisation."""
-    T, H = _dims("x", x, 2)
-    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("weight", weight, (H,), _ACT_TYPES), ("rstd", rstd, (T,), _F32),
-                   ("d_out", d_out, (T, H), _ACT_TYPES), ("d_x", d_x, (T, H), (x.dtype,)),
-                   ("d_weight", d_weight, (H,), _F32))
-    if d_skip is not None:
-        _check_tensors(("d_skip", d_skip, (T, H), (x.dtype,)))
-    _check(_lib.dg_rms_norm_backward(_ptr(d_out), _ptr(d_skip), _ptr(x), _TYPE_CODES[x.dtype], _TYPE_CODES[d_out.dtype],
-                                     _ptr(weight), _TYPE_CODES[weight.dtype], _ptr(rstd), T, H, _ptr(d_x),
-                                     _ptr(d_weight), _raw_stream()))
-
-
-def _norm_params(H, T, y_dtype, weight, weight_post, gate):
-    """(gate kind, type code of the parameters) of a residual norm: weight, weight_post and a gate [H] have one type."""
-    kind = 0 if gate is None else 1 if len(_dims("gate", gate, 1, 2)) == 1 else 2
-    first = weight if weight is not None else weight_post if weight_post is not None else gate if kind == 1 else None
-    dtype = getattr(first, "dtype", torch.float32)
-    if not (dtype in _ACT_TYPES):
-        raise DGError(-1, f"the norms' parameters have dtype {dtype}, expected one of {_ACT_TYPES}")
-    _check_optional(("weight", weight, (H,), (dtype,)), ("weight_post", weight_post, (H,), (dtype,)),
-                    ("gate", gate, (H,) if kind == 1 else (T, H), (dtype,) if kind == 1 else (y_dtype,)))
-    return kind, _TYPE_CODES[dtype]
+    _rowwise.rms_norm_backward(d_out, x, weight, rstd, d_x, d_weight, d_skip)
 
 
 def residual_rms_norm(x: torch.Tensor, y: torch.Tensor, x_out: torch.Tensor, weight: Optional[torch.Tensor] = None, out=None,
@@ -688,19 +527,7 @@ def residual_rms_norm(x: torch.Tensor, y: torch.Tensor, x_out: torch.Tensor, wei
     out = x_out * r_x * weight (weight and out go together).  x and x_out [T, H] bf16 or fp32 (x_out may be x); y [T, H] and
     out bf16 (fp32 with an fp32 x), out also the pair (e4m3, sfa); weight and weight_post [H], gate [H] (one type, bf16 or
     fp32) or [T, H] (y's type).  rstd and rstd_post fp32 [T] keep r_x and r_y for residual_rms_norm_backward."""
-    T, H = _dims("x", x, 2)
-    _check_tensors(("x", x, (T, H), _ACT_TYPES), ("y", y, (T, H), _ACT_TYPES), ("x_out", x_out, (T, H), (x.dtype,)))
-    _check_optional(("rstd", rstd, (T,), _F32), ("rstd_post", rstd_post, (T,), _F32))
-    kind, param_type = _norm_params(H, T, y.dtype, weight, weight_post, gate)
-    _need((weight is None) == (out is None), "weight and out go together")
-    a = sf = None
-    if out is not None:
-        a, sf, _, _ = _row_operand("out", out, H, y.dtype)
-        if not (tuple(a.shape) == (T, H)):
-            raise DGError(-1, f"out must be {[T, H]}, got {list(a.shape)}")
-    _check(_lib.dg_residual_rms_norm(_ptr(x), _TYPE_CODES[x.dtype], _ptr(y), _TYPE_CODES[y.dtype], _ptr(weight),
-                                     _ptr(weight_post), _ptr(gate), kind, param_type, alpha, eps, T, H, _ptr(x_out),
-                                     _ptr(a), _ptr(sf), _ptr(rstd), _ptr(rstd_post), _raw_stream()))
+    _rowwise.residual_rms_norm(x, y, x_out, weight, out, weight_post, gate, alpha, eps, rstd, rstd_post)
 
 
 def residual_rms_norm_backward(d_x_out: Optional[torch.Tensor], y: torch.Tensor, d_x: torch.Tensor, d_y: torch.Tensor,
@@ -713,17 +540,8 @@ def residual_rms_norm_backward(d_x_out: Optional[torch.Tensor], y: torch.Tensor,
     """Gradient of residual_rms_norm.  Comes in: d_x_out (x's type; None: 0) and, with weight, d_out (y's type); x_out as
     the forward stored it, y, the parameters, rstd and rstd_post.  Goes out: d_x (x's type; may be d_x_out), d_y (y's type),
     d_weight and d_weight_post fp32 [H], d_gate fp32 [H] for a gate [H], or of y's type for a gate [T, H]."""
-    T, H = _dims("y", y, 2)
-    _check_tensors(("y", y, (T, H), _ACT_TYPES), ("d_y", d_y, (T, H), (y.dtype,)), ("d_x", d_x, (T, H), _ACT_TYPES))
-    kind, param_type = _norm_params(H, T, y.dtype, weight, weight_post, gate)
-    _check_optional(("d_x_out", d_x_out, (T, H), (d_x.dtype,)), ("d_out", d_out, (T, H), (y.dtype,)),
-                    ("x_out", x_out, (T, H), (d_x.dtype,)), ("rstd", rstd, (T,), _F32), ("rstd_post", rstd_post, (T,), _F32),
-                    ("d_weight", d_weight, (H,), _F32), ("d_weight_post", d_weight_post, (H,), _F32),
-                    ("d_gate", d_gate, (H,) if kind == 1 else (T, H), _F32 if kind == 1 else (y.dtype,)))
-    _check(_lib.dg_residual_rms_norm_backward(
-        _ptr(d_x_out), _ptr(d_out), _ptr(x_out), _TYPE_CODES[d_x.dtype], _ptr(y), _TYPE_CODES[y.dtype], _ptr(weight),
-        _ptr(weight_post), _ptr(gate), kind, param_type, alpha, _ptr(rstd), _ptr(rstd_post), T, H, _ptr(d_x), _ptr(d_y),
-        _ptr(d_weight), _ptr(d_weight_post), _ptr(d_gate), _raw_stream()))
+    _rowwise.residual_rms_norm_backward(d_x_out, y, d_x, d_y, d_out, x_out, weight, rstd, weight_post, rstd_post, gate, alpha,
+                                        d_weight, d_weight_post, d_gate)
 
 
 __all__ = [

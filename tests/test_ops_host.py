@@ -151,18 +151,41 @@ def test_empty_calls_are_no_ops():
     assert L.dg_residual_rms_norm(None, 0, None, 0, B, None, None, 0, 0, z, z, 0, 256, None, None, None, None, None, None) == 0
 
 
-def test_python_refuses_cpu_tensors_and_wrong_shapes():
-    x = torch.zeros(4, 256, dtype=torch.bfloat16)
-    rows = torch.zeros(4, 2, dtype=torch.int32)
-    w = torch.ones(256)
+def test_python_refuses_before_it_needs_a_device():
+    """Types, dimensions, shapes, strides and CPU tensors, each by DGError with DG_ERR_INVALID_ARG."""
+    bf16 = torch.bfloat16
+    x, out = torch.zeros(4, 256, dtype=bf16), torch.zeros(8, 256, dtype=bf16)
+    rows, w, wt = torch.zeros(4, 2, dtype=torch.int32), torch.ones(256), torch.ones(4, 2)
+    f8, sf = torch.zeros(8, 256, dtype=torch.uint8), torch.zeros(2, 8)
+    counts = torch.zeros(3, dtype=torch.int32)
+    calls = {
+        "topk_ids must have 2": lambda: dg.moe_sort_nopad(rows[0], rows, counts),
+        "topk_ids has dtype": lambda: dg.moe_sort_masked(rows.float(), rows, counts, 8),
+        "topk_ids must be a CUDA tensor": lambda: dg.moe_sort_contiguous(rows, rows, counts, counts),
+        "x must be a torch.Tensor": lambda: dg.moe_permute(None, rows, out),
+        "x has dtype": lambda: dg.moe_permute(x.half(), rows, out),
+        "x must be contiguous": lambda: dg.moe_permute(x.t(), rows, out),
+        "x must be a CUDA tensor": lambda: dg.moe_permute(x, rows, out),
+        "rows must have 2 or more dims": lambda: dg.moe_unpermute(x[0], rows, out),
+        "rows must be a CUDA tensor": lambda: dg.moe_unpermute_backward(x, out, rows, wt, out, wt),
+        "gate_up must have 2 or more dims": lambda: dg.swiglu(torch.zeros(4, 2, 3, 2, dtype=bf16), x),
+        "d_out must be a torch.Tensor": lambda: dg.swiglu_backward(None, x, x),
+        "d_x must be a torch.Tensor": lambda: dg.residual_rms_norm_backward(x, x, None, x),
+    }
     if torch.cuda.is_available():
-        with pytest.raises(dg.DGError):
-            dg.moe_permute(x, rows, torch.zeros(8, 256, dtype=torch.bfloat16))
-    for call in (lambda: dg._dims("x", x, 3), lambda: dg._dims("x", None, 2),
-                 lambda: dg.swiglu(torch.zeros(4, 2, 3, 2, dtype=torch.bfloat16), x),
-                 lambda: dg.rms_norm(x, w, torch.zeros(4, 256, dtype=torch.float16))):
-        with pytest.raises(dg.DGError):
+        gx, gr, gw = x.cuda(), rows.cuda(), w.cuda()
+        calls.update({
+            "out must be a tensor or a pair": lambda: dg.moe_permute(gx, gr, (f8, sf, sf)),
+            "out must be a CUDA tensor": lambda: dg.moe_permute(gx, gr, out),
+            "weight and out go together": lambda: dg.residual_rms_norm(gx, gx, gx, weight=gw),
+            "weight must be a torch.Tensor": lambda: dg.residual_rms_norm(gx, gx, gx, weight=3),
+            "eps must be a number": lambda: dg.rms_norm(gx, gw, gx.clone(), eps="a"),
+            "m_max must be an integer": lambda: dg.moe_sort_masked(gr, gr.clone(), gr[0].contiguous(), 1.5),
+        })
+    for message, call in calls.items():
+        with pytest.raises(dg.DGError, match=message) as e:
             call()
+        assert e.value.status == INVALID
 
 
 # ------------------------------------------------------------------------------- the 64-bit forms on small cases
