@@ -24,6 +24,7 @@ constexpr int NORM_MAX_H = 16384;
 constexpr int NORM_MAX_THREADS = 1024;                  // of a CTA whose rows go through shared memory, a vector each
 constexpr int NORM_RING_H = NORM_MAX_THREADS * VEC;     // widest row of such a CTA
 constexpr int NORM_WIDE_THREADS = 512;                  // of a CTA for wider rows
+constexpr int NORM_ROW_WARPS = 8;                       // rows of a forward CTA that takes a row a warp
 constexpr int NORM_MAX_STAGES = 4;
 constexpr int NORM_SHARED_BYTES = 226 * 1024;           // of an SM, for the CTAs' parameters and stages
 enum GateKind { GATE_NONE = 0, GATE_ROW = 1, GATE_TOKEN = 2 };
@@ -47,18 +48,20 @@ __device__ __forceinline__ void load_param(const void *p, int f32, int i, float 
     else load_vec(static_cast<const bf16 *>(p) + i, v);
 }
 
-// Sum over the CTA, the same in every thread.  `part` is read until the next barrier: two buffers in turn.
-__device__ __forceinline__ float cta_sum(float v, float *part) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// Sum over the CTA, the same in every thread.  `part` is read until the next barrier: two buffers in turn.
+__device__ __forceinline__ float cta_sum(float v, float *part) {
+    v = warp_sum(v);
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (warps == 1) return v;
     if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = lane < warps ? part[lane] : 0.f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
+    return warp_sum(lane < warps ? part[lane] : 0.f);
 }
 
 // A thread's vectors in shared memory: the parameters (w, w_post, a gate [H]) and the stages of a row's tensors, in planes of
@@ -273,20 +276,27 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) rms_norm_backward_kernel(con
     }
 }
 
-// One CTA a row, which waits for the sums in registers; ITERS vectors a thread.
-template <typename X, typename Y, bool FP8, int ITERS>
+// A row waits for the sums in registers, ITERS vectors a thread: a row a CTA or, up to 512 columns, a row a WARP, without
+// barriers.
+template <typename X, typename Y, bool FP8, int ITERS, bool WARP>
 __global__ void __launch_bounds__(ITERS == 1 ? NORM_MAX_THREADS : NORM_MAX_H / 32) rms_norm_kernel(const NormParams p) {
     __shared__ float part[2][32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int row = blockIdx.x;
+    const int row = WARP ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && row >= p.T) return;
+    const int lane = WARP ? threadIdx.x & 31 : threadIdx.x, lanes = WARP ? 32 : blockDim.x;  // of the row
+    auto row_sum = [&](float v, float *part) {
+        if constexpr (WARP) return warp_sum(v);
+        else return cta_sum(v, part);
+    };
     const long long at = static_cast<long long>(row) * p.H;
     const float inv_h = 1.f / p.H;
     Raw<X> rx[ITERS];
     Raw<Y> ry[ITERS];
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
-        const int col = (j * blockDim.x + threadIdx.x) * VEC;
+        const int col = (j * lanes + lane) * VEC;
         if (col < p.H) {
             rx[j].load(static_cast<const X *>(p.x) + at + col);
             if (p.y) ry[j].load(static_cast<const Y *>(p.y) + at + col);
@@ -297,18 +307,18 @@ __global__ void __launch_bounds__(ITERS == 1 ? NORM_MAX_THREADS : NORM_MAX_H / 3
         float sum[2] = {};
 #pragma unroll
         for (int j = 0; j < ITERS; ++j)
-            if ((j * blockDim.x + threadIdx.x) * VEC < p.H) {
+            if ((j * lanes + lane) * VEC < p.H) {
                 float n[VEC];
                 ry[j].get(n);
                 dot_vec(sum, n, n);
             }
-        r_post = rsqrtf(fmaf(cta_sum(sum[0] + sum[1], part[0]), inv_h, p.eps));
-        if (threadIdx.x == 0 && p.rstd_post) p.rstd_post[row] = r_post;
+        r_post = rsqrtf(fmaf(row_sum(sum[0] + sum[1], part[0]), inv_h, p.eps));
+        if (lane == 0 && p.rstd_post) p.rstd_post[row] = r_post;
     }
     float x[ITERS][VEC], sum[2] = {};
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
-        const int col = (j * blockDim.x + threadIdx.x) * VEC;
+        const int col = (j * lanes + lane) * VEC;
         if (col >= p.H) continue;
         rx[j].get(x[j]);
         if (p.y) {
@@ -330,11 +340,11 @@ __global__ void __launch_bounds__(ITERS == 1 ? NORM_MAX_THREADS : NORM_MAX_H / 3
         dot_vec(sum, x[j], x[j]);
     }
     if (!p.w) return;
-    const float r = rsqrtf(fmaf(cta_sum(sum[0] + sum[1], part[1]), inv_h, p.eps));
-    if (threadIdx.x == 0 && p.rstd) p.rstd[row] = r;
+    const float r = rsqrtf(fmaf(row_sum(sum[0] + sum[1], part[1]), inv_h, p.eps));
+    if (lane == 0 && p.rstd) p.rstd[row] = r;
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
-        const int col = (j * blockDim.x + threadIdx.x) * VEC;
+        const int col = (j * lanes + lane) * VEC;
         const bool in = col < p.H;  // (the same in a block's lanes where h is e4m3)
         float c[VEC] = {};
         if (in) {
