@@ -64,8 +64,9 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsPara
         float scale[kSteps];
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-            float v[VEC] = {};
-            if (begin + j * STEP < p.H) r[j].get(v);
+            if (begin + j * STEP >= p.H) continue;  // (a block's lanes are in or out together)
+            float v[VEC];
+            r[j].get(v);
             q[j] = quantise(v, block_amax(v), scale[j]);
         }
         for (unsigned m = live; m; m &= m - 1) {
@@ -174,36 +175,31 @@ __global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel
 #pragma unroll
             for (int u = 0; u < GRAD_SLOTS; ++u)
                 if (at[u] >= 0 && in) r[u].load(rows + static_cast<long long>(at[u]) * p.H + col);
-            float d[VEC] = {}, amax = 0.f, keep = 0.f;
-            if (in) load_vec(d_out + col, d);
+            if (!in) continue;  // (a block's lanes are in or out together)
+            float d[VEC], amax = 0.f, keep = 0.f;
+            load_vec(d_out + col, d);
             if constexpr (FP8) amax = block_amax(d);
 #pragma unroll
             for (int u = 0; u < GRAD_SLOTS; ++u)
                 if (at[u] >= 0) {
-                    if (in) {
-                        float v[VEC];
-                        r[u].get(v);
-                        dot_vec(acc[u], d, v);
-                    }
-                    float g[VEC];
+                    float v[VEC];
+                    r[u].get(v);
+                    dot_vec(acc[u], d, v);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) g[i] = d[i];
-                    mul_vec(g, weight[u]);
+                    for (int i = 0; i < VEC; ++i) v[i] = d[i];
+                    mul_vec(v, weight[u]);
                     if constexpr (FP8) {
                         // rounding keeps order: the largest of the rounded products is the product of the largest
                         float scale;
-                        const uint2 q = quantise(g, fabsf(weight[u]) * amax, scale);
+                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + static_cast<long long>(at[u]) * p.H + col) =
+                            quantise(v, fabsf(weight[u]) * amax, scale);
                         if ((lane & 15) == u) keep = scale;
-                        if (in)
-                            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) +
-                                                       static_cast<long long>(at[u]) * p.H + col) = q;
-                    } else if (in) {
-                        store_vec(static_cast<T *>(p.out) + static_cast<long long>(at[u]) * p.H + col, g);
+                    } else {
+                        store_vec(static_cast<T *>(p.out) + static_cast<long long>(at[u]) * p.H + col, v);
                     }
                 }
-            if constexpr (FP8) {
-                if (in && sf) sf[static_cast<long long>(col >> 7) * p.sf.ld] = keep;
-            }
+            if constexpr (FP8)
+                if (sf) sf[static_cast<long long>(col >> 7) * p.sf.ld] = keep;
         }
 #pragma unroll
         for (int u = 0; u < GRAD_SLOTS; ++u) {

@@ -345,21 +345,16 @@ __global__ void __launch_bounds__(ITERS == 1 ? NORM_MAX_THREADS : NORM_MAX_H / 3
 #pragma unroll
     for (int j = 0; j < ITERS; ++j) {
         const int col = (j * lanes + lane) * VEC;
-        const bool in = col < p.H;  // (the same in a block's lanes where h is e4m3)
-        float c[VEC] = {};
-        if (in) {
-            load_param(p.w, p.param_f32, col, c);
-            mul_vec(x[j], r);
-            mul_vec(c, x[j]);
-        }
+        if (col >= p.H) continue;  // (a block's lanes are in or out together)
+        float c[VEC];
+        load_param(p.w, p.param_f32, col, c);
+        mul_vec(x[j], r);
+        mul_vec(c, x[j]);
         if constexpr (FP8) {
             float scale;
-            const uint2 q = quantise(c, block_amax(c), scale);
-            if (in) {
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.h) + at + col) = q;
-                if ((threadIdx.x & (BLOCK_LANES - 1)) == 0) p.sf.sf[static_cast<long long>(col >> 7) * p.sf.ld + row] = scale;
-            }
-        } else if (in) {
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.h) + at + col) = quantise(c, block_amax(c), scale);
+            if ((threadIdx.x & (BLOCK_LANES - 1)) == 0) p.sf.sf[static_cast<long long>(col >> 7) * p.sf.ld + row] = scale;
+        } else {
             store_vec(static_cast<Y *>(p.h) + at + col, c);
         }
     }

@@ -127,6 +127,14 @@ __device__ __forceinline__ void fma_vec(float (&c)[VEC], const float (&a)[VEC], 
 #pragma unroll
     for (int i = 0; i < VEC; i += 2) fma2(c[i], c[i + 1], a[i], a[i + 1], s, s);
 }
+__device__ __forceinline__ void add_vec(float (&a)[VEC], float s) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2)
+        asm("{.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tadd.rn.f32x2 a, a, b;\n\t"
+            "mov.b64 {%0, %1}, a;}"
+            : "+f"(a[i]), "+f"(a[i + 1])
+            : "f"(s));
+}
 // Sum of products of a vector, onto a pair of partial sums.
 __device__ __forceinline__ void dot_vec(float (&sum)[2], const float (&a)[VEC], const float (&b)[VEC]) {
 #pragma unroll

@@ -36,11 +36,10 @@ template <typename T> __device__ __forceinline__ void sigmoid(const float (&g)[V
         for (int i = 0; i < VEC; ++i) s[i] = g[i];
         mul_vec(s, -1.4426950408889634f);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
-            s[i] += 1.f;
-            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
-        }
+        for (int i = 0; i < VEC; ++i) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+        add_vec(s, 1.f);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) s[i] = 1.f / (1.f + expf(-g[i]));
@@ -90,21 +89,18 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS, BACKWARD ? 3 : 4) swiglu_ke
     };
     for (; first < p.cta_rows; first += stride) {
         const unsigned live = owned_rows >> first & ((1u << ROWS) - 1);
-        if (!live) continue;
+        if (!live || !in) continue;  // (`in` is the same in the lanes of a block where the output is e4m3)
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
-            if (in && (live >> r & 1)) load(r);
+            if (live >> r & 1) load(r);
         float keep = 0.f, keep_u = 0.f;  // lane r of a block's lanes: the scale of the block in row r
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
             if (live >> r & 1) {
-                float g[VEC] = {}, u[VEC] = {}, a[VEC], b[VEC];
-                float d[BACKWARD ? VEC : 1] = {};
-                if (in) {
-                    rg[r].get(g);
-                    ru[r].get(u);
-                    if constexpr (BACKWARD) rd[r].get(d);
-                }
+                float g[VEC], u[VEC], a[VEC], b[VEC], d[VEC];
+                rg[r].get(g);
+                ru[r].get(u);
+                if constexpr (BACKWARD) rd[r].get(d);
                 sigmoid<T>(g, a);
                 if constexpr (!BACKWARD) {
                     mul_vec(a, g);
@@ -125,24 +121,23 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS, BACKWARD ? 3 : 4) swiglu_ke
                 if constexpr (FP8) {
                     float scale;
                     uint8_t *out = static_cast<uint8_t *>(p.out) + at;
-                    const uint2 q = quantise(a, block_amax(a), scale);
+                    *reinterpret_cast<uint2 *>(out) = quantise(a, block_amax(a), scale);
                     if ((lane & (BLOCK_LANES - 1)) == r) keep = scale;
-                    if (in) *reinterpret_cast<uint2 *>(out) = q;
                     if constexpr (BACKWARD) {
-                        const uint2 qu = quantise(b, block_amax(b), scale);
+                        *reinterpret_cast<uint2 *>(out + p.I) = quantise(b, block_amax(b), scale);
                         if ((lane & (BLOCK_LANES - 1)) == r) keep_u = scale;
-                        if (in) *reinterpret_cast<uint2 *>(out + p.I) = qu;
                     }
-                } else if (in) {
+                } else {
                     store_vec(static_cast<T *>(p.out) + at, a);
                     if constexpr (BACKWARD) store_vec(static_cast<T *>(p.out) + at + p.I, b);
                 }
             }
         if constexpr (FP8) {
             const int r = lane & (BLOCK_LANES - 1);
-            if (in && r < ROWS && (live >> r & 1)) {
-                *p.sf.at(row0 + first + r, col >> 7) = keep;
-                if constexpr (BACKWARD) *p.sf.at(row0 + first + r, (p.I + col) >> 7) = keep_u;
+            if (r < ROWS && (live >> r & 1)) {
+                float *sf = p.own_kind == OWN_MASKED ? p.sf.at(row0 + first + r, 0) : p.sf.sf + row0 + first + r;
+                sf[static_cast<long long>(col >> 7) * p.sf.ld] = keep;
+                if constexpr (BACKWARD) sf[static_cast<long long>((p.I + col) >> 7) * p.sf.ld] = keep_u;
             }
         }
     }
