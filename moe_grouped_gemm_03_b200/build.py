@@ -11,9 +11,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdg.so")
 BINDING = os.path.join(HERE, "_rowwise.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.cu", "moe_ops.cu")]
+SOURCES = [os.path.join(CSRC, "libdg.cu")]
 BINDING_SOURCE = os.path.join(CSRC, "rowwise_binding.cpp")
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))] + \
     [os.path.join(INCLUDE, "dg.h")]
 BINDING_DEPS = [BINDING_SOURCE, os.path.join(INCLUDE, "dg.h")]
 
@@ -62,8 +62,7 @@ def build_binding() -> None:
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or not _newer(LIB, DEPS):
         tmp = LIB + ".tmp"
-        # the sources are compiled side by side (they share no device code), then linked
-        cmd = [nvcc()] + flags(verbose) + ["--threads", str(len(SOURCES))] + SOURCES + ["-o", tmp]
+        cmd = [nvcc()] + flags(verbose) + SOURCES + ["-o", tmp]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
     if force or not _newer(BINDING, BINDING_DEPS):

@@ -12,7 +12,6 @@
 #include <string>
 
 #include "dg.h"
-#include "dg_internal.h"
 #include "gemm_kernel.cuh"
 #include "scale_pack.cuh"
 #include "transpose.cuh"
@@ -909,32 +908,6 @@ int masked_call(const void *a, const float *sfa, const void *b, const float *sfb
 }
 
 }  // namespace
-
-// What the other translation units use (dg_internal.h).
-namespace dg {
-
-int fail(int code, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return code;
-}
-int cuda_fail(cudaError_t e, const char *what) { return ::cuda_fail(e, what); }
-int current_device(int &device, int &num_sms) {
-    DeviceInfo info;
-    if (int rc = device_info(info)) return rc;
-    device = info.device;
-    num_sms = effective_sms(info);
-    return DG_OK;
-}
-int scratch_pool(int device, cudaMemPool_t &pool) { return ::scratch_pool(device, pool); }
-unsigned *device_error_word() { return ::device_error_word(); }
-int contiguous_alignment() { return g_m_alignment.load(); }
-
-}  // namespace dg
 
 extern "C" {
 

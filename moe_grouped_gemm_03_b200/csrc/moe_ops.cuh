@@ -1,12 +1,7 @@
 // Host side of the operators around the grouped GEMMs (include/dg.h): argument validation and launches of dispatch,
-// combine, SwiGLU and the norms on the caller's stream.
-#include <cuda_runtime.h>
-
-#include <cmath>
-#include <cstdint>
-
-#include "dg.h"
-#include "dg_internal.h"
+// combine, SwiGLU and the norms on the caller's stream.  Compiled behind dg_api.cu (libdg.cu), whose errors, device
+// information, scratch pool and settings it uses.
+#pragma once
 #include "moe_rows.cuh"
 #include "moe_sort.cuh"
 #include "rms_norm.cuh"
@@ -15,16 +10,22 @@
 namespace {
 
 using dg::bf16;
-using dg::cuda_fail;
-using dg::fail;
 
 constexpr int kMaxRows = 1 << 30;  // rows and tokens of a call: row arithmetic stays within 32 bits
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 // Vectors of eight elements: 16 bytes of bf16, 32 of fp32.
 bool vec_aligned(const void *p, int type) { return aligned(p, type == DG_F32 ? 32 : 16); }
 bool is_type(int t) { return t == DG_BF16 || t == DG_F32; }
 int aligned_rows(int rows) { return (rows + 3) / 4 * 4; }
+
+// The current device (an sm_100) and its SMs under the cap of dg_set_num_sms.
+int current_device(int &device, int &num_sms) {
+    DeviceInfo info;
+    if (int rc = device_info(info)) return rc;
+    device = info.device;
+    num_sms = effective_sms(info);
+    return DG_OK;
+}
 
 // Launches `kernel` as a programmatic dependent: it may be set up while the kernel before it on the stream ends, and
 // waits for that one (griddepcontrol.wait) before it touches memory.  Every kernel of this file does so at its start.
@@ -79,9 +80,9 @@ template <typename Id, bool ONE> int launch_sort(const dg::SortParams &p, int wa
 
 int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) {
     int device, sms;
-    if (int rc = dg::current_device(device, sms)) return rc;
+    if (int rc = current_device(device, sms)) return rc;
     p.slots = T * k;
-    p.err = dg::device_error_word();
+    p.err = device_error_word();
     if (!p.err) return fail(DG_ERR_CUDA, "device error word is not available");
     int warps = (p.slots + 31) / 32;
     // Measured (us, 256 groups, one CTA / 8 / 16): 256 slots 2.9 / 3.8 / -, 1024 slots 6.2 / 3.8 / -, 2048 slots
@@ -132,7 +133,7 @@ int scale_layout(dg::ScaleLayout &sf, float *out_sf, int rows, int rows_per_grou
 
 int rows_params(dg::RowsParams &p, const void *x, const int *row_of_slot, int T, int k, int H, int rows, void *out) {
     int device, sms;
-    if (int rc = dg::current_device(device, sms)) return rc;
+    if (int rc = current_device(device, sms)) return rc;
     p.x = x;
     p.row_of_slot = row_of_slot;
     p.T = T;
@@ -140,7 +141,7 @@ int rows_params(dg::RowsParams &p, const void *x, const int *row_of_slot, int T,
     p.H = H;
     p.rows = rows;
     p.out = out;
-    p.err = dg::device_error_word();
+    p.err = device_error_word();
     return p.err ? DG_OK : fail(DG_ERR_CUDA, "device error word is not available");
 }
 
@@ -200,7 +201,7 @@ int swiglu_call(dg::SwigluParams p, int type, bool backward, const int *m_indice
     if (int rc = scale_layout(p.sf, out_sf, p.R, p.rows_per_group, (backward ? 2 : 1) * p.I)) return rc;
     if (p.R == 0) return DG_OK;
     int device, sms;
-    if (int rc = dg::current_device(device, sms)) return rc;
+    if (int rc = current_device(device, sms)) return rc;
     if (type == DG_BF16) {
         if (backward) return out_sf ? launch_swiglu<bf16, true, true>(p, stream) : launch_swiglu<bf16, false, true>(p, stream);
         return out_sf ? launch_swiglu<bf16, true, false>(p, stream) : launch_swiglu<bf16, false, false>(p, stream);
@@ -294,7 +295,7 @@ int norm_call(const dg::NormParams &p, int x_type, int y_type, int param_type, d
     if (int rc = check_norm(p, x_type, y_type, param_type)) return rc;
     if (p.T == 0) return DG_OK;
     int device, sms;
-    if (int rc = dg::current_device(device, sms)) return rc;
+    if (int rc = current_device(device, sms)) return rc;
     if (x_type == DG_BF16) return launch_norm<bf16, bf16>(p, sms, stream);
     return y_type == DG_BF16 ? launch_norm<float, bf16>(p, sms, stream) : launch_norm<float, float>(p, sms, stream);
 }
@@ -334,14 +335,14 @@ int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type,
         return DG_OK;
     }
     int device, sms;
-    if (int rc = dg::current_device(device, sms)) return rc;
+    if (int rc = current_device(device, sms)) return rc;
     const NormShape shape = x_type == DG_BF16   ? norm_backward_shape<bf16, bf16>(p, sms)
                             : y_type == DG_BF16 ? norm_backward_shape<float, bf16>(p, sms)
                                                 : norm_backward_shape<float, float>(p, sms);
     const int ctas = shape.ctas;
     p.stages = shape.stages;
     cudaMemPool_t pool;
-    if (int rc = dg::scratch_pool(device, pool)) return rc;
+    if (int rc = scratch_pool(device, pool)) return rc;
     void *partial = nullptr;
     e = cudaMallocFromPoolAsync(&partial, sizeof(float) * 3 * p.H * static_cast<size_t>(ctas), pool, s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync (parameter gradients)");
@@ -364,7 +365,7 @@ extern "C" {
 
 long long dg_moe_m_total_bound(long long num_slots, int G) {
     if (num_slots < 0 || G < 1) return fail(DG_ERR_INVALID_ARG, "num_slots=%lld and G=%d are out of range", num_slots, G);
-    const long long a = dg::contiguous_alignment();
+    const long long a = dg_get_m_alignment_for_contiguous_layout();
     return (num_slots + (num_slots < G ? num_slots : G) * (a - 1)) / a * a;
 }
 
@@ -373,7 +374,7 @@ int dg_moe_sort_contiguous(const void *topk_ids, int id_bytes, int T, int k, int
     if (int rc = check_sort(topk_ids, id_bytes, T, k, G, row_of_slot, counts)) return rc;
     if (!m_indices && M_total > 0) return fail(DG_ERR_INVALID_ARG, "m_indices is null");
     if (!aligned(m_indices, 16)) return fail(DG_ERR_ALIGNMENT, "m_indices must be 16-byte aligned");
-    const int a = dg::contiguous_alignment();
+    const int a = dg_get_m_alignment_for_contiguous_layout();
     if (M_total < 0 || M_total > kMaxRows) return fail(DG_ERR_INVALID_ARG, "M_total=%d must be in [0, 2^30]", M_total);
     if (M_total % a) return fail(DG_ERR_ALIGNMENT, "M_total=%d must be a multiple of %d", M_total, a);
     dg::SortParams p{};

@@ -66,6 +66,9 @@ __device__ __forceinline__ unsigned same_expert(int id, int bits) {
     return same;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ int load_shared_rank(const int *p, int rank) {
     int v;
     asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(map_shared_rank(smem_u32(p), rank)) : "memory");
