@@ -264,7 +264,8 @@ DG_EXPORT int dg_moe_sort_masked(const void *topk_ids, int id_bytes, int T, int 
 
 /* Dispatch: out[row_of_slot[t][s]] = x[t] for every slot with a row.  x [T][H] of `type`; out [rows][H] (masked:
  * rows = G * M_max) of the same type, or e4m3 with out_sf.  row_of_slot names a row at most once; a row outside
- * [-1, rows) is skipped and recorded as DG_ERR_BAD_GROUP.  Its gradient is dg_moe_unpermute without weights. */
+ * [-1, rows) is skipped and recorded as DG_ERR_BAD_GROUP.  H <= 2^24.  Its gradient is dg_moe_unpermute
+ * without weights. */
 DG_EXPORT int dg_moe_permute(const void *x, int type, const int *row_of_slot, int T, int k, int H, int rows,
                              int rows_per_group, void *out, float *out_sf, dg_stream_t stream);
 
@@ -274,7 +275,8 @@ DG_EXPORT int dg_moe_unpermute(const void *rows_in, int type, const int *row_of_
                                int H, int rows, void *out, dg_stream_t stream);
 
 /* Gradient of the combine: d_rows[row_of_slot[t][s]] = weights[t][s] * d_out[t] (of `type`, or e4m3 with d_rows_sf) and
- * d_weights[t][s] = <d_out[t], rows_in[row_of_slot[t][s]]> (0 for a slot without a row). */
+ * d_weights[t][s] = <d_out[t], rows_in[row_of_slot[t][s]]> (0 for a slot without a row).  row_of_slot names a row at most
+ * once. */
 DG_EXPORT int dg_moe_unpermute_backward(const void *d_out, const void *rows_in, int type, const int *row_of_slot,
                                         const float *weights, int T, int k, int H, int rows, int rows_per_group,
                                         void *d_rows, float *d_rows_sf, float *d_weights, dg_stream_t stream);

@@ -111,7 +111,7 @@ int check_rows(const void *x, const int *row_of_slot, const void *out, const flo
     if (T < 0 || T > kMaxRows || rows < 0 || rows > kMaxRows)
         return fail(DG_ERR_INVALID_ARG, "T=%d and rows=%d must be in [0, 2^30]", T, rows);
     if (k < 1 || k > dg::MAX_TOPK) return fail(DG_ERR_INVALID_ARG, "k=%d must be in [1, %d]", k, dg::MAX_TOPK);
-    if (H <= 0) return fail(DG_ERR_INVALID_ARG, "H=%d must be positive", H);
+    if (H <= 0 || H > (1 << 24)) return fail(DG_ERR_INVALID_ARG, "H=%d must be in [1, 2^24]", H);
     if (H % dg::VEC) return fail(DG_ERR_ALIGNMENT, "H=%d must be a multiple of %d", H, dg::VEC);
     if (!vec_aligned(x, type) || !vec_aligned(out, out_sf ? DG_BF16 : type))
         return fail(DG_ERR_ALIGNMENT, "row operands must be 16-byte (fp32: 32-byte) aligned");

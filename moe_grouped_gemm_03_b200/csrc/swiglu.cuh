@@ -55,13 +55,13 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS, BACKWARD ? 3 : 4) swiglu_ke
     int valid = p.R;  // no padding: rows that the counts cover (negative counts are none)
     if (p.own_kind == OWN_COUNTS) {
         int n = 0;
-        for (int g = threadIdx.x; g < p.G; g += blockDim.x) n = min(n + max(p.own[g], 0), p.R);
+        for (int g = threadIdx.x; g < p.G; g += blockDim.x) n += min(max(p.own[g], 0), p.R - n);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) n = min(n + __shfl_xor_sync(0xffffffffu, n, d), p.R);
+        for (int d = 16; d > 0; d >>= 1) n += min(__shfl_xor_sync(0xffffffffu, n, d), p.R - n);
         if (lane == 0) part[warp] = n;
         __syncthreads();
         valid = 0;
-        for (int i = 0; i < SWIGLU_WARPS; ++i) valid = min(valid + part[i], p.R);
+        for (int i = 0; i < SWIGLU_WARPS; ++i) valid += min(part[i], p.R - valid);
     }
     // The CTA's rows, and which of them are rows of a group (a bit each).
     const int row0 = blockIdx.x * p.cta_rows;

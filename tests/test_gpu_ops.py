@@ -424,6 +424,9 @@ def test_swiglu_masked_counts_out_of_range(dg):
     dg.swiglu(gu.view(30, 256), out.out, counts=torch.tensor([2 ** 31 - 1, 2 ** 31 - 1, 5], dtype=torch.int32, device="cuda"))
     want = ref.swiglu(gu.cpu().view(30, 256)).numpy()
     out.check(np.arange(30), want, np.abs(want) * 2.0 ** -17)
+    out = Operand((30, 128), BF16, False)  # the sum of 1024 counts far past 32 bits
+    dg.swiglu(gu.view(30, 256), out.out, counts=torch.full((1024,), 2 ** 31 - 1, dtype=torch.int32, device="cuda"))
+    out.check(np.arange(30), want, np.abs(want) * 2.0 ** -17)
 
 
 # --------------------------------------------------------------------------------------------------------- norms
@@ -719,6 +722,68 @@ def test_two_captured_graphs_replay_in_turn(dg):
         torch.cuda.synchronize()
         for (_, o, _), w in zip(sets, want):
             assert all(torch.equal(o[k], w[k]) for k in o), trial
+    dg.check_device_error()
+
+
+@pytest.mark.parametrize("T", [40, 200, 900])  # one CTA, clusters of 8 and of 16
+def test_captured_sort_replays(dg, T):
+    """Every launch shape of the sort in a graph, replayed on other ids."""
+    g, G, k = gen(T), 300, 4
+    ids = torch.randint(-1, G, (T, k), device="cuda", generator=g)
+    M = dg.get_m_total_bound(T * k, G)
+    new = lambda *s: torch.full(s, -99, dtype=torch.int32, device="cuda")  # noqa: E731
+    rows, m, counts = new(T, k), new(M), new(G)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        dg.moe_sort_contiguous(ids, rows, m, counts)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            dg.moe_sort_contiguous(ids, rows, m, counts)
+    torch.cuda.current_stream().wait_stream(s)
+    for trial in range(2):
+        ids.copy_(torch.randint(-1, G, (T, k), device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.sort(ids.cpu().numpy(), "contiguous", G, m_total=M)
+        for a, b in zip((rows, counts, m), want):
+            assert (a.cpu().numpy() == b).all()
+    dg.check_device_error()
+
+
+def test_calls_from_two_threads(dg):
+    """Two host threads, each on its own stream with its own tensors, at once: each gets what it gets alone."""
+    import threading
+
+    sets = [_calls(dg, seed) for seed in (3, 4)]
+    want = []
+    for _, o, run in sets:
+        run()
+        torch.cuda.synchronize()
+        want.append(_bits(o))
+        for v in o.values():
+            v.zero_()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(run):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    run()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(run,)) for _, _, run in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for (_, o, _), w in zip(sets, want):
+        assert all(torch.equal(o[k], w[k]) for k in o)
     dg.check_device_error()
 
 
