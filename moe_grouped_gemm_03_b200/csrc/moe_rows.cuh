@@ -138,26 +138,29 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) unpermute_kernel(const RowsPa
     if (in) store_vec(static_cast<T *>(p.out) + token * p.H + col, acc);
 }
 
-constexpr int GRAD_SLOTS = 8;       // slots of a token at a time
 constexpr int GRAD_MAX_WARPS = 16;
 
-// One CTA a token: the inner products need whole rows.  fp32 sums, in an order that does not change.
-template <typename T, bool FP8>
-__global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel(const RowsParams p) {
-    __shared__ float part[GRAD_SLOTS][GRAD_MAX_WARPS];
+// The inner products need whole rows: a CTA a token or, with many tokens, a WARP a token, which needs no barrier and lets a
+// short row's latency be covered by other tokens.  SLOTS of a token at a time, their loads together.  fp32 sums, in an order
+// that does not change.
+template <typename T, bool FP8, int SLOTS, bool WARP>
+__global__ void __launch_bounds__(32 * (WARP ? ROWS_WARPS : GRAD_MAX_WARPS), WARP ? 2 : 1)
+    unpermute_backward_kernel(const RowsParams p) {
+    __shared__ float part[SLOTS][GRAD_MAX_WARPS];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const long long token = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = WARP ? 0 : threadIdx.x >> 5, warps = WARP ? 1 : blockDim.x >> 5;
+    const long long token = WARP ? static_cast<long long>(blockIdx.x) * ROWS_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && token >= p.T) return;
     const int row = slot_row(p, token, lane);
-    const float w = lane < p.k ? *(p.weights + token * p.k + lane) : 0.f;
+    const float w = lane < p.k ? p.weights[token * p.k + lane] : 0.f;
     const T *d_out = static_cast<const T *>(p.d_out) + token * p.H;
     const T *rows = static_cast<const T *>(p.x);
-    for (int first = 0; first < p.k; first += GRAD_SLOTS) {
-        int at[GRAD_SLOTS];
-        float weight[GRAD_SLOTS], acc[GRAD_SLOTS][2] = {};
+    for (int first = 0; first < p.k; first += SLOTS) {
+        int at[SLOTS];
+        float weight[SLOTS], acc[SLOTS][2] = {};
 #pragma unroll
-        for (int u = 0; u < GRAD_SLOTS; ++u) {
+        for (int u = 0; u < SLOTS; ++u) {
             at[u] = __shfl_sync(0xffffffffu, row, (first + u) & 31);
             if (first + u >= p.k) at[u] = -1;
             weight[u] = __shfl_sync(0xffffffffu, w, (first + u) & 31);
@@ -166,21 +169,18 @@ __global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel
         float *sf = nullptr;
         if constexpr (FP8) {
             const int mine = __shfl_sync(0xffffffffu, row, (first + (lane & 15)) & 31);
-            if ((lane & 15) < GRAD_SLOTS && first + (lane & 15) < p.k && mine >= 0) sf = p.sf.at(mine, 0);
+            if ((lane & 15) < SLOTS && first + (lane & 15) < p.k && mine >= 0) sf = p.sf.at(mine, 0);
         }
-        for (int base = warp * STEP; base < p.H; base += warps * STEP) {
-            const int col = base + lane * VEC;
-            const bool in = col < p.H;
-            Raw<T> r[GRAD_SLOTS];
+        for (int col = warp * STEP + lane * VEC; col < p.H; col += warps * STEP) {  // (a block's lanes end together)
+            Raw<T> r[SLOTS];
 #pragma unroll
-            for (int u = 0; u < GRAD_SLOTS; ++u)
-                if (at[u] >= 0 && in) r[u].load(rows + static_cast<long long>(at[u]) * p.H + col);
-            if (!in) continue;  // (a block's lanes are in or out together)
+            for (int u = 0; u < SLOTS; ++u)
+                if (at[u] >= 0) r[u].load(rows + static_cast<long long>(at[u]) * p.H + col);
             float d[VEC], amax = 0.f, keep = 0.f;
             load_vec(d_out + col, d);
             if constexpr (FP8) amax = block_amax(d);
 #pragma unroll
-            for (int u = 0; u < GRAD_SLOTS; ++u)
+            for (int u = 0; u < SLOTS; ++u)
                 if (at[u] >= 0) {
                     float v[VEC];
                     r[u].get(v);
@@ -201,20 +201,27 @@ __global__ void __launch_bounds__(32 * GRAD_MAX_WARPS) unpermute_backward_kernel
             if constexpr (FP8)
                 if (sf) sf[static_cast<long long>(col >> 7) * p.sf.ld] = keep;
         }
+        __syncwarp();
 #pragma unroll
-        for (int u = 0; u < GRAD_SLOTS; ++u) {
+        for (int u = 0; u < SLOTS; ++u) {
             float sum = acc[u][0] + acc[u][1];
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (lane == 0) part[u][warp] = sum;
+            if (WARP) {
+                if (lane == 0 && first + u < p.k) p.d_weights[token * p.k + first + u] = sum;
+            } else if (lane == 0) {
+                part[u][warp] = sum;
+            }
         }
-        __syncthreads();
-        if (threadIdx.x < GRAD_SLOTS && first + threadIdx.x < p.k) {
-            float sum = 0.f;
-            for (int i = 0; i < warps; ++i) sum += part[threadIdx.x][i];
-            p.d_weights[token * p.k + first + threadIdx.x] = sum;
+        if (!WARP) {
+            __syncthreads();
+            if (threadIdx.x < SLOTS && first + threadIdx.x < p.k) {
+                float sum = 0.f;
+                for (int i = 0; i < warps; ++i) sum += part[threadIdx.x][i];
+                p.d_weights[token * p.k + first + threadIdx.x] = sum;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
