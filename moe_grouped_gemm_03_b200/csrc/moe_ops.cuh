@@ -286,15 +286,18 @@ int launch_norm_ring(const char *name, void (*kernel)(dg::NormParams), const dg:
 }
 
 template <typename X, typename Y, bool FP8> int launch_norm(const dg::NormParams &p, int sms, dg_stream_t stream) {
-    // few rows: as many threads a row as there can be, the call is one row long; many: 32 elements a thread, so that fewer
-    // warps take part in the sums (8192 x 7168: 131 us with 32 or 16 elements a thread, 195 us with 8)
+    // 8 elements a thread while all rows' vectors fit on the SMs together (the call is then one row long), 16 up to twice that
+    // (667 x 5120: 13 us, 18 with 32), then 32, so that fewer warps take part in the sums (8192 x 7168: 131 us with 32 or
+    // 16 elements a thread, 195 us with 8)
     const int vecs = p.H / dg::VEC;
-    if (p.T <= sms && vecs <= dg::NORM_MAX_THREADS)
-        return launch("norm launch", dg::rms_norm_kernel<X, Y, FP8, 1, false>, dim3(static_cast<unsigned>(p.T)),
-                      dim3((vecs + 31) / 32 * 32), 0, 1, stream, p);
-    if (vecs > 64)
-        return launch("norm launch", dg::rms_norm_kernel<X, Y, FP8, 4, false>, dim3(static_cast<unsigned>(p.T)),
-                      dim3(((vecs + 3) / 4 + 31) / 32 * 32), 0, 1, stream, p);
+    const long long vecs_per_sm = (p.T * static_cast<long long>(vecs) + sms - 1) / sms;
+    const int iters = vecs > dg::NORM_MAX_THREADS ? 4 : vecs_per_sm <= 1024 || p.T <= sms ? 1 : vecs_per_sm <= 4096 ? 2 : 4;
+    if (vecs > 64 || iters == 1) {
+        auto kernel = iters == 1   ? dg::rms_norm_kernel<X, Y, FP8, 1, false>
+                      : iters == 2 ? dg::rms_norm_kernel<X, Y, FP8, 2, false> : dg::rms_norm_kernel<X, Y, FP8, 4, false>;
+        return launch("norm launch", kernel, dim3(static_cast<unsigned>(p.T)), dim3(((vecs + iters - 1) / iters + 31) / 32 * 32),
+                      0, 1, stream, p);
+    }
     // a row a warp: 16384 rows of 256 in 8 us (18 with a row a CTA), of 512 in 16 (21), of 1024 in 28 (29) but 36 (33) in e4m3
     auto kernel = vecs <= 32 ? dg::rms_norm_kernel<X, Y, FP8, 1, true> : dg::rms_norm_kernel<X, Y, FP8, 2, true>;
     return launch("norm launch", kernel, dim3((p.T + dg::NORM_ROW_WARPS - 1) / dg::NORM_ROW_WARPS),
@@ -319,9 +322,8 @@ template <typename X, typename Y> NormShape norm_backward_shape(const dg::NormPa
     const int units = dg::norm_stage_units(dg::Raw<X>::UNITS, dg::Raw<Y>::UNITS, p.w != nullptr, p.y != nullptr,
                                            p.gate_kind == dg::GATE_TOKEN);
     const int threads = (p.H / dg::VEC + 31) / 32 * 32;
-    // at 64 registers; more than 8 CTAs an SM would add more to the sums over the CTAs than they save
-    const int per_sm = dg::NORM_MAX_THREADS / threads;
-    return norm_shape(p, units, per_sm > 8 ? 8 : per_sm, sms);
+    const int per_sm = dg::NORM_MAX_THREADS / threads;  // (at 64 registers)
+    return norm_shape(p, units, per_sm, sms);
 }
 
 template <typename X, typename Y> int launch_norm_backward(const dg::NormParams &p, const NormShape &s, dg_stream_t stream) {
@@ -363,10 +365,14 @@ int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type,
     int rc = x_type == DG_BF16   ? launch_norm_backward<bf16, bf16>(p, shape, stream)
              : y_type == DG_BF16 ? launch_norm_backward<float, bf16>(p, shape, stream)
                                  : launch_norm_backward<float, float>(p, shape, stream);
-    if (rc == DG_OK && (d_w || d_w_post || d_gate_row))
-        rc = launch("norm gradient sum launch", dg::rms_norm_sum_kernel,
-                    dim3((p.H + 4 * dg::NORM_SUM_LANES - 1) / (4 * dg::NORM_SUM_LANES), 3),
-                    dim3(dg::NORM_SUM_LANES, dg::NORM_SUM_PARTS), 0, 1, stream, static_cast<const float *>(p.partial), ctas, p.H, d_w, d_w_post, d_gate_row);
+    if (rc == DG_OK && (d_w || d_w_post || d_gate_row)) {
+        // columns of a CTA: 64, or 16 for short rows, whose sums would be the work of a few SMs (1184 partial sums of 288: 11 us)
+        const bool narrow = p.H <= 2048;
+        const int cols = narrow ? 16 : 64;
+        rc = launch("norm gradient sum launch", narrow ? dg::rms_norm_sum_kernel<4> : dg::rms_norm_sum_kernel<16>,
+                    dim3((p.H + cols - 1) / cols, 3), dim3(dg::NORM_SUM_THREADS), 0, 1, stream,
+                    static_cast<const float *>(p.partial), ctas, p.H, d_w, d_w_post, d_gate_row);
+    }
     e = cudaFreeAsync(partial, s);
     if (rc == DG_OK && e != cudaSuccess) rc = cuda_fail(e, "cudaFreeAsync (parameter gradients)");
     return rc;

@@ -102,13 +102,14 @@ struct NormSlots {
         v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
         v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
     }
-    // parameter number i
+    // parameter number i; through L1: up to 32 CTAs of an SM start on the same few lines, and all SMs' requests for them meet in
+    // a few slices of L2 (8192 x 640 with w in fp32: 16 us, 32 when the copies pass L1 by; 8192 x 1024, all parameters: 27, 42)
     __device__ __forceinline__ void copy_param(int i, const void *src, int f32, int col) const {
         if (f32) {
-            copy_async16(unit(2 * i), static_cast<const float *>(src) + col);
-            copy_async16(unit(2 * i + 1), static_cast<const float *>(src) + col + 4);
+            copy_async16_ca(unit(2 * i), static_cast<const float *>(src) + col);
+            copy_async16_ca(unit(2 * i + 1), static_cast<const float *>(src) + col + 4);
         } else {
-            copy_async16(unit(i), static_cast<const bf16 *>(src) + col);
+            copy_async16_ca(unit(i), static_cast<const bf16 *>(src) + col);
         }
     }
     __device__ __forceinline__ void get_param(int i, int f32, float (&v)[VEC]) const {
@@ -479,32 +480,42 @@ __global__ void __launch_bounds__(NORM_WIDE_THREADS) rms_norm_backward_wide_kern
     }
 }
 
-constexpr int NORM_SUM_LANES = 16, NORM_SUM_PARTS = 64;  // lanes of four columns; parts of the CTAs
+constexpr int NORM_SUM_THREADS = 1024;
 
-// d[z][col] = sum over the CTAs' partial sums, in an order that does not change.  blockIdx.y: which of the three.
-__global__ void __launch_bounds__(NORM_SUM_LANES *NORM_SUM_PARTS)
+// d[z][col] = sum over the CTAs' partial sums, in an order that does not change.  blockIdx.y: which of the three.  LANES lanes
+// of four columns, the CTAs' sums in 1024 / LANES parts.
+template <int LANES>
+__global__ void __launch_bounds__(NORM_SUM_THREADS)
     rms_norm_sum_kernel(const float *partial, int ctas, int H, float *d0, float *d1, float *d2) {
-    __shared__ float4 part[NORM_SUM_PARTS][NORM_SUM_LANES];
+    constexpr int kParts = NORM_SUM_THREADS / LANES;
+    __shared__ float4 part[NORM_SUM_THREADS / 32][LANES];
     grid_dependency_wait();
     grid_launch_dependents();
     float *d = blockIdx.y == 0 ? d0 : blockIdx.y == 1 ? d1 : d2;
     if (!d) return;
-    const int col = (blockIdx.x * NORM_SUM_LANES + threadIdx.x) * 4;  // (H is a multiple of 8)
+    const int lane = threadIdx.x % LANES;
+    const int col = (blockIdx.x * LANES + lane) * 4;  // (H is a multiple of 8)
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < H)
 #pragma unroll 4
-        for (int b = threadIdx.y; b < ctas; b += NORM_SUM_PARTS) {
+        for (int b = threadIdx.x / LANES; b < ctas; b += kParts) {
             const float4 v = *reinterpret_cast<const float4 *>(partial + (static_cast<long long>(b) * 3 + blockIdx.y) * H + col);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
-    part[threadIdx.y][threadIdx.x] = sum;
+#pragma unroll
+    for (int i = LANES; i < 32; i *= 2) {
+        sum.x += __shfl_xor_sync(0xffffffffu, sum.x, i);
+        sum.y += __shfl_xor_sync(0xffffffffu, sum.y, i);
+        sum.z += __shfl_xor_sync(0xffffffffu, sum.z, i);
+        sum.w += __shfl_xor_sync(0xffffffffu, sum.w, i);
+    }
+    if ((threadIdx.x & 31) < LANES) part[threadIdx.x >> 5][lane] = sum;
     __syncthreads();
-    const int t = threadIdx.y * NORM_SUM_LANES + threadIdx.x;  // a thread a column
-    const int out = blockIdx.x * NORM_SUM_LANES * 4 + t;
-    if (t < NORM_SUM_LANES * 4 && out < H) {
+    const int out = blockIdx.x * LANES * 4 + threadIdx.x;  // a thread a column
+    if (threadIdx.x < LANES * 4 && out < H) {
         float s = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < NORM_SUM_PARTS; ++i) s += reinterpret_cast<const float *>(part[i])[t];
+#pragma unroll
+        for (int w = 0; w < NORM_SUM_THREADS / 32; ++w) s += reinterpret_cast<const float *>(part[w])[threadIdx.x];
         d[out] = s;
     }
 }

@@ -33,6 +33,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ void copy_async16(void *s, const void *p) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s)), "l"(p) : "memory");
 }
+// (through L1: what several CTAs of an SM read)
+__device__ __forceinline__ void copy_async16_ca(void *s, const void *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s)), "l"(p) : "memory");
+}
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_async_wait() {  // until at most N groups are under way
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

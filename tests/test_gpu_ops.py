@@ -294,6 +294,14 @@ def test_unpermute_backward(dg, T, k, H, shape, dtype, fp8):
     near(d_w.reshape(-1), want, size * 96 * 2.0 ** -24 + want * 0)
 
 
+@pytest.mark.parametrize("T,k,H,shape,dtype,fp8", [(1201, 1, 128, (1500,), F32, True), (1190, 3, 2176, (4, 1000), BF16, True),
+                                                   (1300, 8, 384, (11000,), BF16, False), (1185, 11, 640, (14000,), F32, False),
+                                                   (1187, 2, 1152, (2400,), BF16, True)])
+def test_unpermute_backward_of_many_tokens(dg, T, k, H, shape, dtype, fp8):
+    """From 8 tokens an SM on a warp takes a token: the sums' chains are as long as those above."""
+    test_unpermute_backward(dg, T, k, H, shape, dtype, fp8)
+
+
 def test_unpermute_gradient_against_differences(dg):
     """<d_out, out(w + h e) - out(w - h e)> / 2h and the same for the rows: the combine is linear in each, so the
     difference is the gradient but for the fp32 roundings of the two outputs."""
@@ -555,6 +563,22 @@ def test_rms_norm_backward(dg, T, H, X, Y):
     in_place = skip.clone()  # the gradient that comes in past the norm may be the buffer that goes out
     dg.rms_norm_backward(do, t["x"], t["w"], r, in_place, d_w, d_skip=in_place)
     assert torch.equal(in_place, d_x)
+
+
+# more rows than the SMs take at once: a row a warp, 16 or 32 elements a thread; a gradient's CTAs take several rows each, more
+# than are copied ahead, and their sums for a parameter are chains of at most 11 + 19 + 3 + 32 additions
+@pytest.mark.parametrize("X,Y", TYPES)
+@pytest.mark.parametrize("T,H", [(50000, 8), (4800, 256), (2500, 512), (1500, 1288), (1600, 4104)])
+def test_norms_of_many_rows(dg, T, H, X, Y):
+    test_rms_norm(dg, T, H, X, Y)
+    test_rms_norm_backward(dg, T, H, X, Y)
+
+
+@pytest.mark.parametrize("X,Y,gate,T,H", [(BF16, BF16, "token", 1600, 4104), (F32, BF16, "row", 2500, 512), (F32, F32, "none", 4800, 256),
+                                          (BF16, BF16, "row", 50000, 8), (F32, F32, "token", 1500, 1288)])
+def test_residual_norms_of_many_rows(dg, X, Y, gate, T, H):
+    test_residual_rms_norm(dg, T, H, gate, X, Y)
+    test_residual_rms_norm_backward(dg, T, H, gate, X, Y)
 
 
 def test_norm_gradient_against_differences(dg):
