@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) permute_kernel(const RowsPara
             if (begin + j * STEP >= p.H) continue;  // (a block's lanes are in or out together)
             float v[VEC];
             r[j].get(v);
-            q[j] = quantise(v, block_amax(v), scale[j]);
+            q[j] = quantise(v, block_amax(v, begin + j * STEP, p.H), scale[j]);
         }
         for (unsigned m = live; m; m &= m - 1) {
             const long long at = __shfl_sync(0xffffffffu, row, __ffs(m) - 1);
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(32 * (WARP ? ROWS_WARPS : GRAD_MAX_WARPS), WAR
                 if (at[u] >= 0) r[u].load(rows + static_cast<long long>(at[u]) * p.H + col);
             float d[VEC], amax = 0.f, keep = 0.f;
             load_vec(d_out + col, d);
-            if constexpr (FP8) amax = block_amax(d);
+            if constexpr (FP8) amax = block_amax(d, col, p.H);
 #pragma unroll
             for (int u = 0; u < SLOTS; ++u)
                 if (at[u] >= 0) {

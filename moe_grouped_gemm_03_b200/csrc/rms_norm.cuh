@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(ITERS == 1 ? NORM_MAX_THREADS : NORM_MAX_H / 3
         mul_vec(c, x[j]);
         if constexpr (FP8) {
             float scale;
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.h) + at + col) = quantise(c, block_amax(c), scale);
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.h) + at + col) = quantise(c, block_amax(c, col, p.H), scale);
             if ((threadIdx.x & (BLOCK_LANES - 1)) == 0) p.sf.sf[static_cast<long long>(col >> 7) * p.sf.ld + row] = scale;
         } else {
             store_vec(static_cast<Y *>(p.h) + at + col, c);

@@ -122,10 +122,10 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS, BACKWARD ? 3 : 4) swiglu_ke
                 if constexpr (FP8) {
                     float scale;
                     uint8_t *out = static_cast<uint8_t *>(p.out) + at;
-                    *reinterpret_cast<uint2 *>(out) = quantise(a, block_amax(a), scale);
+                    *reinterpret_cast<uint2 *>(out) = quantise(a, block_amax(a, col, p.I), scale);
                     if ((lane & (BLOCK_LANES - 1)) == r) keep = scale;
                     if constexpr (BACKWARD) {
-                        *reinterpret_cast<uint2 *>(out + p.I) = quantise(b, block_amax(b), scale);
+                        *reinterpret_cast<uint2 *>(out + p.I) = quantise(b, block_amax(b, col, p.I), scale);
                         if ((lane & (BLOCK_LANES - 1)) == r) keep_u = scale;
                     }
                 } else {
