@@ -286,12 +286,15 @@ int launch_norm_ring(const char *name, void (*kernel)(dg::NormParams), const dg:
 }
 
 template <typename X, typename Y, bool FP8> int launch_norm(const dg::NormParams &p, int sms, dg_stream_t stream) {
-    // 8 elements a thread while all rows' vectors fit on the SMs together (the call is then one row long), 16 up to twice that
-    // (667 x 5120: 13 us, 18 with 32), then 32, so that fewer warps take part in the sums (8192 x 7168: 131 us with 32 or
-    // 16 elements a thread, 195 us with 8)
+    // 8 elements a thread while all rows' vectors fit on the SMs together (the call is then one row long); with many rows 32, so
+    // that fewer warps take part in the sums (bf16, 8192 x 8192: 92 us, 113 with 16), but 16 up to 16 times what fits (4000 x
+    // 4096: 32 us, 33 with 32; 1344 x 5888: 22, 23) and with fp32 outputs, whose rows wait longer for memory (8192 x 8192: 139
+    // us, 151 with 32; 1344 x 5888: 27, 32)
     const int vecs = p.H / dg::VEC;
     const long long vecs_per_sm = (p.T * static_cast<long long>(vecs) + sms - 1) / sms;
-    const int iters = vecs > dg::NORM_MAX_THREADS ? 4 : vecs_per_sm <= 1024 || p.T <= sms ? 1 : vecs_per_sm <= 4096 ? 2 : 4;
+    const int iters = vecs > dg::NORM_MAX_THREADS                   ? 4
+                      : vecs_per_sm <= 1024 || p.T <= sms           ? 1
+                      : vecs_per_sm <= 16 * 1024 || sizeof(Y) == 4 ? 2 : 4;
     if (vecs > 64 || iters == 1) {
         auto kernel = iters == 1   ? dg::rms_norm_kernel<X, Y, FP8, 1, false>
                       : iters == 2 ? dg::rms_norm_kernel<X, Y, FP8, 2, false> : dg::rms_norm_kernel<X, Y, FP8, 4, false>;
@@ -330,9 +333,10 @@ template <typename X, typename Y> int launch_norm_backward(const dg::NormParams 
     if (p.H > dg::NORM_RING_H)
         return launch("norm gradient launch", dg::rms_norm_backward_wide_kernel<X, Y, 4>, dim3(s.ctas), dim3(s.threads), 0, 1,
                       stream, p);
-    auto kernel = p.gate_kind == dg::GATE_NONE  ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE>
-                  : p.gate_kind == dg::GATE_ROW ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_ROW>
-                                                : dg::rms_norm_backward_kernel<X, Y, dg::GATE_TOKEN>;
+    auto kernel = !p.y                           ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE, false>
+                  : p.gate_kind == dg::GATE_NONE ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE, true>
+                  : p.gate_kind == dg::GATE_ROW  ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_ROW, true>
+                                                 : dg::rms_norm_backward_kernel<X, Y, dg::GATE_TOKEN, true>;
     return launch_norm_ring("norm gradient launch", kernel, p, s, stream);
 }
 
