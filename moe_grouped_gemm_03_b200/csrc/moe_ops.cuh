@@ -264,7 +264,9 @@ NormShape norm_shape(const dg::NormParams &p, int stage_units, int per_sm, int s
     NormShape s{};
     s.threads = (p.H / dg::VEC + 31) / 32 * 32;
     const int unit = 16 * s.threads, param_bytes = dg::norm_param_units(p.param_f32, p.gate_kind) * unit, stage_bytes = stage_units * unit;
-    auto stages = [&](int n) { return (dg::NORM_SHARED_BYTES / n - 1024 - param_bytes) / stage_bytes; };
+    // (1 KB of a CTA is the system's, 256 bytes its static ones: left out, 32 CTAs an SM did not all fit, 128905 x 256 in fp32 98 us
+    // in place of 80)
+    auto stages = [&](int n) { return (dg::NORM_SHARED_BYTES / n - 1280 - param_bytes) / stage_bytes; };
     while (per_sm > 1 && stages(per_sm) < 2) --per_sm;
     s.ctas = p.T < per_sm * sms ? p.T : per_sm * sms;
     s.stages = stages(per_sm);
