@@ -254,7 +254,10 @@ int gate_of(const void *gate, int kind) {
 }
 
 // Launch of the kernels whose rows go through shared memory: CTAs of a vector a thread, as many an SM as `per_sm` and the
-// shared memory allow, with up to four stages each; one CTA fewer where that leaves no second stage.
+// shared memory allow, with up to four stages each.  More than four CTAs: one fewer where that gives a second stage (fp32, 512
+// columns, y and a gate for each token: 168 us, 187 without); of up to four none is given up for it (fp32 stream with y and a gate
+// [H], 4096 columns: 107 us, 154 with one CTA and more stages; 2048 columns: 102 and 112; but with bf16 and fp32 parameters 85
+// and 80).
 struct NormShape {
     int threads, ctas, stages;
     size_t smem;
@@ -267,7 +270,7 @@ NormShape norm_shape(const dg::NormParams &p, int stage_units, int per_sm, int s
     // (1 KB of a CTA is the system's, 256 bytes its static ones: left out, 32 CTAs an SM did not all fit, 128905 x 256 in fp32 98 us
     // in place of 80)
     auto stages = [&](int n) { return (dg::NORM_SHARED_BYTES / n - 1280 - param_bytes) / stage_bytes; };
-    while (per_sm > 1 && stages(per_sm) < 2) --per_sm;
+    while (per_sm > 1 && stages(per_sm) < (per_sm > 4 ? 2 : 1)) --per_sm;
     s.ctas = p.T < per_sm * sms ? p.T : per_sm * sms;
     s.stages = stages(per_sm);
     const int rows = (p.T + s.ctas - 1) / s.ctas;  // (of a CTA: more stages would stay empty)
