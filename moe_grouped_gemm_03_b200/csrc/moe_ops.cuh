@@ -49,6 +49,18 @@ int launch(const char *name, void (*kernel)(Params...), dim3 grid, dim3 block, s
     return e == cudaSuccess ? DG_OK : cuda_fail(e, name);
 }
 
+// Lets `Kernel` have `bytes` of dynamic shared memory, the most that any call of it asks for, once per kernel and device.  The
+// attribute belongs to the function and is shared by all host threads: set by each call to its own size, it could be lowered by
+// another thread's smaller call before the launch, which the runtime then refuses.
+template <auto Kernel> int allow_shared(int device, int bytes, const char *what) {
+    static std::atomic<bool> set[64];
+    if (device < 64 && set[device].load(std::memory_order_acquire)) return DG_OK;
+    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    if (device < 64) set[device].store(true, std::memory_order_release);
+    return DG_OK;
+}
+
 // ------------------------------------------------------------------------------------------------ dispatch: rows
 int check_sort(const void *topk_ids, int id_bytes, int T, int k, int G, const int *row_of_slot, const int *counts) {
     if (!counts || (T > 0 && (!topk_ids || !row_of_slot))) return fail(DG_ERR_INVALID_ARG, "null pointer argument");
@@ -64,18 +76,15 @@ int check_sort(const void *topk_ids, int id_bytes, int T, int k, int G, const in
     return DG_OK;
 }
 
-template <typename Id, bool ONE> int launch_sort(const dg::SortParams &p, int warps, int ctas, dg_stream_t stream) {
+template <typename Id, bool ONE> int launch_sort(const dg::SortParams &p, int warps, int ctas, int device, dg_stream_t stream) {
+    constexpr auto kernel = dg::moe_sort_kernel<Id, ONE>;
+    constexpr int kMostShared = static_cast<int>(sizeof(int)) * dg::sort_smem_words(dg::SORT_MAX_WARPS, dg::SORT_MAX_GROUPS);
+    if (int rc = allow_shared<kernel>(device, kMostShared, "cudaFuncSetAttribute (sort)")) return rc;
     const size_t smem = sizeof(int) * dg::sort_smem_words(p.slot_warps, p.G);
-    // notes on the kernel, made anew by each call that needs them: more than 48 KB, a cluster of more than 8
-    cudaError_t e;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(dg::moe_sort_kernel<Id, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem))) != cudaSuccess)
-        return cuda_fail(e, "cudaFuncSetAttribute (sort)");
-    if (ctas > 8 && (e = cudaFuncSetAttribute(dg::moe_sort_kernel<Id, ONE>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                              1)) != cudaSuccess)
+    cudaError_t e;  // (a note that a cluster may have more than 8 CTAs: no other call takes it back)
+    if (ctas > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
         return cuda_fail(e, "cudaFuncSetAttribute (sort cluster)");
-    return launch("sort launch", dg::moe_sort_kernel<Id, ONE>, dim3(ctas), dim3(32 * warps), smem, ctas, stream, p);
+    return launch("sort launch", kernel, dim3(ctas), dim3(32 * warps), smem, ctas, stream, p);
 }
 
 int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) {
@@ -98,8 +107,9 @@ int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) 
     warps = p.slot_warps > group_warps ? p.slot_warps : group_warps;
     const bool one = p.per_warp <= 32 * dg::SORT_BATCHES;
     if (id_bytes == 8)
-        return one ? launch_sort<long long, true>(p, warps, ctas, stream) : launch_sort<long long, false>(p, warps, ctas, stream);
-    return one ? launch_sort<int, true>(p, warps, ctas, stream) : launch_sort<int, false>(p, warps, ctas, stream);
+        return one ? launch_sort<long long, true>(p, warps, ctas, device, stream)
+                   : launch_sort<long long, false>(p, warps, ctas, device, stream);
+    return one ? launch_sort<int, true>(p, warps, ctas, device, stream) : launch_sort<int, false>(p, warps, ctas, device, stream);
 }
 
 // ----------------------------------------------------------------------------------------- dispatch and combine
@@ -267,9 +277,8 @@ NormShape norm_shape(const dg::NormParams &p, int stage_units, int per_sm, int s
     NormShape s{};
     s.threads = (p.H / dg::VEC + 31) / 32 * 32;
     const int unit = 16 * s.threads, param_bytes = dg::norm_param_units(p.param_f32, p.gate_kind) * unit, stage_bytes = stage_units * unit;
-    // (1 KB of a CTA is the system's, 256 bytes its static ones: left out, 32 CTAs an SM did not all fit, 128905 x 256 in fp32 98 us
-    // in place of 80)
-    auto stages = [&](int n) { return (dg::NORM_SHARED_BYTES / n - 1280 - param_bytes) / stage_bytes; };
+    // (with NORM_CTA_BYTES left out, 32 CTAs an SM did not all fit, 128905 x 256 in fp32 98 us in place of 80)
+    auto stages = [&](int n) { return (dg::NORM_SHARED_BYTES / n - dg::NORM_CTA_BYTES - param_bytes) / stage_bytes; };
     while (per_sm > 1 && stages(per_sm) < (per_sm > 4 ? 2 : 1)) --per_sm;
     s.ctas = p.T < per_sm * sms ? p.T : per_sm * sms;
     s.stages = stages(per_sm);
@@ -280,14 +289,9 @@ NormShape norm_shape(const dg::NormParams &p, int stage_units, int per_sm, int s
     return s;
 }
 
-int launch_norm_ring(const char *name, void (*kernel)(dg::NormParams), const dg::NormParams &p, const NormShape &s,
-                     dg_stream_t stream) {
-    cudaError_t e;
-    // (48 KB without being told so, the kernel's static 256 bytes among them)
-    if (s.smem > 47 * 1024 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                        static_cast<int>(s.smem))) != cudaSuccess)
-        return cuda_fail(e, "cudaFuncSetAttribute (norm)");
-    return launch(name, kernel, dim3(s.ctas), dim3(s.threads), s.smem, 1, stream, p);
+template <auto Kernel> int launch_norm_ring(const dg::NormParams &p, const NormShape &s, int device, dg_stream_t stream) {
+    if (int rc = allow_shared<Kernel>(device, dg::NORM_SHARED_BYTES - dg::NORM_CTA_BYTES, "cudaFuncSetAttribute (norm)")) return rc;
+    return launch("norm gradient launch", Kernel, dim3(s.ctas), dim3(s.threads), s.smem, 1, stream, p);
 }
 
 template <typename X, typename Y, bool FP8> int launch_norm(const dg::NormParams &p, int sms, dg_stream_t stream) {
@@ -334,15 +338,17 @@ template <typename X, typename Y> NormShape norm_backward_shape(const dg::NormPa
     return norm_shape(p, units, per_sm, sms);
 }
 
-template <typename X, typename Y> int launch_norm_backward(const dg::NormParams &p, const NormShape &s, dg_stream_t stream) {
+template <typename X, typename Y>
+int launch_norm_backward(const dg::NormParams &p, const NormShape &s, int device, dg_stream_t stream) {
     if (p.H > dg::NORM_RING_H)
         return launch("norm gradient launch", dg::rms_norm_backward_wide_kernel<X, Y, 4>, dim3(s.ctas), dim3(s.threads), 0, 1,
                       stream, p);
-    auto kernel = !p.y                           ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE, false>
-                  : p.gate_kind == dg::GATE_NONE ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE, true>
-                  : p.gate_kind == dg::GATE_ROW  ? dg::rms_norm_backward_kernel<X, Y, dg::GATE_ROW, true>
-                                                 : dg::rms_norm_backward_kernel<X, Y, dg::GATE_TOKEN, true>;
-    return launch_norm_ring("norm gradient launch", kernel, p, s, stream);
+    if (!p.y) return launch_norm_ring<dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE, false>>(p, s, device, stream);
+    if (p.gate_kind == dg::GATE_NONE)
+        return launch_norm_ring<dg::rms_norm_backward_kernel<X, Y, dg::GATE_NONE, true>>(p, s, device, stream);
+    if (p.gate_kind == dg::GATE_ROW)
+        return launch_norm_ring<dg::rms_norm_backward_kernel<X, Y, dg::GATE_ROW, true>>(p, s, device, stream);
+    return launch_norm_ring<dg::rms_norm_backward_kernel<X, Y, dg::GATE_TOKEN, true>>(p, s, device, stream);
 }
 
 int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type, float *d_w, float *d_w_post,
@@ -371,9 +377,9 @@ int norm_backward_call(dg::NormParams p, int x_type, int y_type, int param_type,
     e = cudaMallocFromPoolAsync(&partial, sizeof(float) * 3 * p.H * static_cast<size_t>(ctas), pool, s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync (parameter gradients)");
     p.partial = static_cast<float *>(partial);
-    int rc = x_type == DG_BF16   ? launch_norm_backward<bf16, bf16>(p, shape, stream)
-             : y_type == DG_BF16 ? launch_norm_backward<float, bf16>(p, shape, stream)
-                                 : launch_norm_backward<float, float>(p, shape, stream);
+    int rc = x_type == DG_BF16   ? launch_norm_backward<bf16, bf16>(p, shape, device, stream)
+             : y_type == DG_BF16 ? launch_norm_backward<float, bf16>(p, shape, device, stream)
+                                 : launch_norm_backward<float, float>(p, shape, device, stream);
     if (rc == DG_OK && (d_w || d_w_post || d_gate_row)) {
         // columns of a CTA: 64, or 16 for short rows, whose sums would be the work of a few SMs (1184 partial sums of 288: 11 us)
         const bool narrow = p.H <= 2048;

@@ -27,6 +27,7 @@ constexpr int NORM_WIDE_THREADS = 512;                  // of a CTA for wider ro
 constexpr int NORM_ROW_WARPS = 8;                       // rows of a forward CTA that takes a row a warp
 constexpr int NORM_MAX_STAGES = 4;
 constexpr int NORM_SHARED_BYTES = 226 * 1024;           // of an SM, for the CTAs' parameters and stages
+constexpr int NORM_CTA_BYTES = 1024 + 256;              // of them a CTA's for the system and its static ones
 enum GateKind { GATE_NONE = 0, GATE_ROW = 1, GATE_TOKEN = 2 };
 
 struct NormParams {

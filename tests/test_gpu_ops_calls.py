@@ -1,0 +1,155 @@
+"""Calls of the operators around the grouped GEMMs as concurrent and captured programs make them: C callers on several host
+threads, one graph of calls of several sizes."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import _ops_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dg():
+    import moe_grouped_gemm_03_b200 as dg
+
+    return dg
+
+
+def at_once(*works):
+    """Runs each callable on a host thread of its own and CUDA stream, all begun together; raises the first error."""
+    torch.cuda.synchronize()
+    errors, begin = [], threading.Barrier(len(works))
+
+    def body(work):
+        try:
+            stream = torch.cuda.Stream()
+            begin.wait()
+            with torch.cuda.stream(stream):
+                work(stream.cuda_stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=body, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if errors:
+        raise errors[0]
+
+
+class NormGradient:
+    """residual_rms_norm_backward with a gate [H] on T rows, by its C entry point (ctypes leaves the interpreter's lock)."""
+
+    def __init__(self, dg, T, H, seed):
+        self.dg, self.T, self.H = dg, T, H
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s, dtype=BF16: torch.randn(*s, device="cuda", generator=g).to(dtype)  # noqa: E731
+        self.inputs = dict(d_x_out=r(T, H), d_out=r(T, H), x_out=r(T, H), y=r(T, H), weight=r(H), weight_post=r(H), gate=r(H),
+                           rstd=torch.ones(T, device="cuda"), rstd_post=torch.ones(T, device="cuda"))
+        self.d_x, self.d_y = torch.zeros_like(self.inputs["y"]), torch.zeros_like(self.inputs["y"])
+        self.d_w, self.d_wp, self.d_gate = torch.zeros(3, H, device="cuda")
+
+    def outputs(self):
+        return [self.d_x, self.d_y, self.d_w, self.d_wp, self.d_gate]
+
+    def __call__(self, stream):
+        p = {k: v.data_ptr() for k, v in self.inputs.items()}
+        rc = self.dg.lib().dg_residual_rms_norm_backward(
+            p["d_x_out"], p["d_out"], p["x_out"], 0, p["y"], 0, p["weight"], p["weight_post"], p["gate"], 1, 0, 1.0, p["rstd"],
+            p["rstd_post"], self.T, self.H, self.d_x.data_ptr(), self.d_y.data_ptr(), self.d_w.data_ptr(), self.d_wp.data_ptr(),
+            self.d_gate.data_ptr(), stream)
+        assert rc == 0, (self.H, rc, self.dg.last_error())
+
+
+class Sort:
+    """moe_sort_nopad of n tokens over G groups by its C entry point."""
+
+    def __init__(self, dg, n, G, seed):
+        self.dg, self.n, self.G = dg, n, G
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.ids = torch.randint(-1, G, (n, 4), device="cuda", generator=g, dtype=torch.int32)
+        self.rows, self.counts = torch.zeros_like(self.ids), torch.zeros(G, dtype=torch.int32, device="cuda")
+
+    def outputs(self):
+        return [self.rows, self.counts]
+
+    def __call__(self, stream):
+        rc = self.dg.lib().dg_moe_sort_nopad(self.ids.data_ptr(), 4, self.n, 4, self.G, self.rows.data_ptr(),
+                                             self.counts.data_ptr(), stream)
+        assert rc == 0, (self.G, rc, self.dg.last_error())
+
+
+def alone(calls):
+    """What each call gives by itself; its outputs are zeros afterwards."""
+    want = []
+    for c in calls:
+        c(torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        want.append([v.clone() for v in c.outputs()])
+        for v in c.outputs():
+            v.zero_()
+    return want
+
+
+def same(calls, want):
+    return all(torch.equal(a, b) for c, w in zip(calls, want) for a, b in zip(c.outputs(), w))
+
+
+def pairs(dg):
+    """Calls of one kernel that want different amounts of shared memory."""
+    return {"norm": [NormGradient(dg, 600, 7168, 1), NormGradient(dg, 600, 4096, 2)],
+            "sort": [Sort(dg, 8000, 1024, 3), Sort(dg, 8000, 400, 4)]}
+
+
+@pytest.mark.parametrize("kind", ["norm", "sort"])
+def test_two_threads_with_different_sizes(dg, kind):
+    """A kernel's shared memory is not what another thread's smaller call of it left: no valid call is refused."""
+    calls = pairs(dg)[kind]
+    want = alone(calls)
+
+    def many(call):
+        def work(stream):
+            for _ in range(10000):
+                call(stream)
+
+        return work
+
+    at_once(*[many(c) for c in calls])
+    assert same(calls, want)
+    dg.check_device_error()
+
+
+@pytest.mark.parametrize("kind", ["norm", "sort"])
+def test_one_graph_with_different_sizes(dg, kind):
+    """The wide call first, the narrow one behind it, both in one graph."""
+    calls = pairs(dg)[kind]
+    want = alone(calls)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        for c in calls:
+            c(torch.cuda.current_stream().cuda_stream)
+    for _ in range(2):
+        for c in calls:
+            for v in c.outputs():
+                v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(calls, want)
+    dg.check_device_error()
+
+
+def test_sorts_of_threads_against_the_plain_form(dg):
+    """(what `alone` compares with is right)"""
+    call = Sort(dg, 500, 1024, 5)
+    call(torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    rows, counts, _ = ref.sort(call.ids.cpu().numpy(), "nopad", call.G)
+    assert (call.rows.cpu().numpy() == rows).all() and (call.counts.cpu().numpy() == np.asarray(counts)).all()
