@@ -50,9 +50,12 @@ struct DeviceInfo {
 int device_info(DeviceInfo &info) {
     cudaError_t e = cudaGetDevice(&info.device);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    // the attributes of a device do not change: queried once per device
+    // The attributes of a device do not change: queried once per device.  An entry is read only once it is complete (0: empty,
+    // 1: being written by the thread that took it, 2: complete), so that two threads' first calls cannot see half of one.
     static DeviceInfo cache[64];
-    if (info.device >= 0 && info.device < 64 && cache[info.device].device == info.device) {
+    static std::atomic<int> state[64];
+    const bool cached = info.device >= 0 && info.device < 64;
+    if (cached && state[info.device].load(std::memory_order_acquire) == 2) {
         info = cache[info.device];
         return DG_OK;
     }
@@ -65,7 +68,11 @@ int device_info(DeviceInfo &info) {
     if (info.major != 10 || info.minor != 0)
         return fail(DG_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a only", info.device,
                     info.major, info.minor);
-    if (info.device >= 0 && info.device < 64) cache[info.device] = info;
+    int empty = 0;
+    if (cached && state[info.device].compare_exchange_strong(empty, 1)) {
+        cache[info.device] = info;
+        state[info.device].store(2, std::memory_order_release);
+    }
     return DG_OK;
 }
 

@@ -1,5 +1,8 @@
 """Calls of the operators around the grouped GEMMs as concurrent and captured programs make them: C callers on several host
 threads, one graph of calls of several sizes."""
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -144,6 +147,30 @@ def test_one_graph_with_different_sizes(dg, kind):
         torch.cuda.synchronize()
         assert same(calls, want)
     dg.check_device_error()
+
+
+def test_first_calls_of_a_process_from_many_threads(dg):
+    """Eight host threads make their first call of the library in a new process at once."""
+    code = """
+import threading, torch
+import moe_grouped_gemm_03_b200 as dg
+x = torch.randn(64, 512, device="cuda"); w = torch.ones(512, device="cuda")
+outs = [torch.zeros_like(x) for _ in range(8)]
+torch.cuda.synchronize()
+begin, bad, L = threading.Barrier(8), [], dg.lib()
+def work(o):
+    begin.wait()
+    rc = L.dg_rms_norm(x.data_ptr(), 1, w.data_ptr(), 1, 1e-6, 64, 512, o.data_ptr(), 1, None, None, None)
+    if rc: bad.append(dg.last_error())
+ts = [threading.Thread(target=work, args=(o,)) for o in outs]
+[t.start() for t in ts]; [t.join() for t in ts]
+torch.cuda.synchronize()
+assert not bad, bad
+assert all(torch.equal(o, outs[0]) for o in outs) and float(outs[0].abs().sum()) > 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_sorts_of_threads_against_the_plain_form(dg):
