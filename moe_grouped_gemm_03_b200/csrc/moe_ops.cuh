@@ -76,15 +76,48 @@ int check_sort(const void *topk_ids, int id_bytes, int T, int k, int G, const in
     return DG_OK;
 }
 
-template <typename Id, bool ONE> int launch_sort(const dg::SortParams &p, int warps, int ctas, int device, dg_stream_t stream) {
+// Makes one of the sort's kernels ready on the current device: its shared memory, and clusters of more than 8 CTAs.  `most`
+// becomes the largest of 16, 8 and 1 CTAs (or stays, if smaller) whose cluster the device can place with the most shared memory
+// and threads that a call asks for: 16 CTAs need as many free SMs in one GPC, which a part of a GPU may not have.
+template <typename Id, bool ONE> int prepare_sort(int device, int &most) {
     constexpr auto kernel = dg::moe_sort_kernel<Id, ONE>;
     constexpr int kMostShared = static_cast<int>(sizeof(int)) * dg::sort_smem_words(dg::SORT_MAX_WARPS, dg::SORT_MAX_GROUPS);
     if (int rc = allow_shared<kernel>(device, kMostShared, "cudaFuncSetAttribute (sort)")) return rc;
-    const size_t smem = sizeof(int) * dg::sort_smem_words(p.slot_warps, p.G);
-    cudaError_t e;  // (a note that a cluster may have more than 8 CTAs: no other call takes it back)
-    if (ctas > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-        return cuda_fail(e, "cudaFuncSetAttribute (sort cluster)");
-    return launch("sort launch", kernel, dim3(ctas), dim3(32 * warps), smem, ctas, stream, p);
+    if (most > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) most = 8;
+    for (; most > 1; most = most > 8 ? 8 : 1) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(most);
+        cfg.blockDim = dim3(32 * dg::SORT_MAX_WARPS);
+        cfg.dynamicSmemBytes = kMostShared;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(most);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0) break;
+    }
+    cudaGetLastError();  // (what the runtime refused here is no error of the call)
+    return DG_OK;
+}
+
+// The most CTAs of a sort's cluster on this device, found by its first sort.
+int sort_most_ctas(int device, int &most) {
+    static std::atomic<int> cache[64];
+    if (device < 64 && (most = cache[device].load(std::memory_order_acquire)) > 0) return DG_OK;
+    most = dg::SORT_MAX_CTAS;
+    int rc = prepare_sort<int, true>(device, most);
+    if (!rc) rc = prepare_sort<int, false>(device, most);
+    if (!rc) rc = prepare_sort<long long, true>(device, most);
+    if (!rc) rc = prepare_sort<long long, false>(device, most);
+    if (!rc && device < 64) cache[device].store(most, std::memory_order_release);
+    return rc;
+}
+
+template <typename Id, bool ONE> int launch_sort(const dg::SortParams &p, int warps, int ctas, dg_stream_t stream) {
+    return launch("sort launch", dg::moe_sort_kernel<Id, ONE>, dim3(ctas), dim3(32 * warps),
+                  sizeof(int) * dg::sort_smem_words(p.slot_warps, p.G), ctas, stream, p);
 }
 
 int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) {
@@ -96,7 +129,12 @@ int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) 
     int warps = (p.slots + 31) / 32;
     // Measured (us, 256 groups, one CTA / 8 / 16): 256 slots 2.9 / 3.8 / -, 1024 slots 6.2 / 3.8 / -, 2048 slots
     // 7.0 / 3.9 / 3.9, 8192 slots - / 5.3 / 4.3, 65536 slots - / 10.4 / 7.9.
-    const int ctas = warps > 32 ? 16 : warps > 8 ? 8 : 1;
+    int ctas = warps > 32 ? 16 : warps > 8 ? 8 : 1, most;
+    if (int rc = sort_most_ctas(device, most)) return rc;
+    if (most > sms) most = sms;  // (the cap of dg_set_num_sms: a sort's CTAs take an SM each)
+    if (ctas > most) ctas = most >= 8 ? 8 : 1;
+    static const bool debug = getenv("DG_DEBUG") && getenv("DG_DEBUG")[0] == '1';
+    if (debug) fprintf(stderr, "[dg] sort layout=%d slots=%d G=%d ctas=%d\n", p.layout, p.slots, p.G, ctas);
     warps = (warps + ctas - 1) / ctas;
     p.slot_warps = warps < 1 ? 1 : warps > dg::SORT_MAX_WARPS ? dg::SORT_MAX_WARPS : warps;
     const int all = p.slot_warps * ctas;
@@ -107,9 +145,8 @@ int sort_call(dg::SortParams p, int id_bytes, int T, int k, dg_stream_t stream) 
     warps = p.slot_warps > group_warps ? p.slot_warps : group_warps;
     const bool one = p.per_warp <= 32 * dg::SORT_BATCHES;
     if (id_bytes == 8)
-        return one ? launch_sort<long long, true>(p, warps, ctas, device, stream)
-                   : launch_sort<long long, false>(p, warps, ctas, device, stream);
-    return one ? launch_sort<int, true>(p, warps, ctas, device, stream) : launch_sort<int, false>(p, warps, ctas, device, stream);
+        return one ? launch_sort<long long, true>(p, warps, ctas, stream) : launch_sort<long long, false>(p, warps, ctas, stream);
+    return one ? launch_sort<int, true>(p, warps, ctas, stream) : launch_sort<int, false>(p, warps, ctas, stream);
 }
 
 // ----------------------------------------------------------------------------------------- dispatch and combine

@@ -180,3 +180,40 @@ def test_sorts_of_threads_against_the_plain_form(dg):
     torch.cuda.synchronize()
     rows, counts, _ = ref.sort(call.ids.cpu().numpy(), "nopad", call.G)
     assert (call.rows.cpu().numpy() == rows).all() and (call.counts.cpu().numpy() == np.asarray(counts)).all()
+
+
+SORT_UNDER_CAP = """
+import sys, torch
+import moe_grouped_gemm_03_b200 as dg
+(T, k, G), kind, caps = map(int, sys.argv[1:4]), getattr(torch, sys.argv[4]), map(int, sys.argv[5:])
+g = torch.Generator(device="cuda").manual_seed(T)
+ids = torch.randint(-1, G, (T, k), device="cuda", generator=g).to(kind)
+def run():
+    rows, counts = torch.full((T, k), -9, dtype=torch.int32, device="cuda"), torch.full((G,), -9, dtype=torch.int32, device="cuda")
+    dg.moe_sort_nopad(ids, rows, counts)
+    m, n = torch.full((dg.get_m_total_bound(T * k, G),), -9, dtype=torch.int32, device="cuda"), torch.empty_like(counts)
+    at = torch.empty_like(rows)
+    dg.moe_sort_contiguous(ids, at, m, n)
+    torch.cuda.synchronize()
+    return rows, counts, at, m, n
+want = run()
+for cap in caps:
+    dg.set_num_sms(cap)
+    assert all(torch.equal(a, b) for a, b in zip(want, run())), cap
+dg.check_device_error()
+flat, (rows, counts) = ids.view(-1).long(), want[:2]
+order = torch.argsort(torch.where(flat < 0, G, flat), stable=True)[: int(counts.sum())]
+assert torch.equal(rows.view(-1)[order], torch.arange(len(order), device="cuda", dtype=torch.int32)) and int((rows >= 0).sum()) == len(order)
+"""
+
+
+@pytest.mark.parametrize("T,k,G,kind", [(20000, 8, 1024, "int64"), (1100, 1, 5, "int32")])
+def test_sort_takes_no_more_sms_than_the_cap(T, k, G, kind):
+    """The plan that DG_DEBUG=1 prints has a cluster that fits under set_num_sms; the rows do not depend on it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    clusters = {16: 16, 15: 8, 8: 8, 7: 1, 1: 1, 0: 16}
+    done = subprocess.run([sys.executable, "-c", SORT_UNDER_CAP, *map(str, (T, k, G, kind, *clusters))], cwd=root,
+                          capture_output=True, text=True, timeout=300, env=dict(os.environ, DG_DEBUG="1"))
+    assert done.returncode == 0, done.stderr[-2000:]
+    plans = [int(line.rsplit("ctas=", 1)[1]) for line in done.stderr.splitlines() if line.startswith("[dg] sort")]
+    assert plans == [n for n in (16, *clusters.values()) for _ in range(2)]  # (both layouts)
