@@ -1,7 +1,7 @@
 // Python binding of the row-wise operators (dispatch, combine, SwiGLU, norms): a CPython module that checks torch tensors and
 // calls the C entry points of include/dg.h.  These calls last a few microseconds on the GPU, about as long as the checks of
 // their arguments take in Python; here a tensor is checked in about 50 ns.  It holds no arithmetic and no state but the error
-// class it is given.
+// class it is given.  The entry points themselves run without the interpreter's lock.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/cuda/CUDAFunctions.h>
@@ -110,6 +110,15 @@ int size(const at::Tensor &t, int d) { return static_cast<int>(t.size(d)); }
 template <typename T = void> T *ptr(const at::Tensor &t) { return static_cast<T *>(t.data_ptr()); }
 template <typename T = void> T *ptr(const at::Tensor *t) { return t ? static_cast<T *>(t->data_ptr()) : nullptr; }
 
+// The C call, its arguments already made, without the interpreter's lock: a launch waits where the queue of launches is full, and
+// what drains the queue may be a callback that needs the lock.  (The caller holds its tensors until the call returns.)
+template <typename F, typename... Args> int without_lock(F f, Args... args) {
+    PyThreadState *state = PyEval_SaveThread();
+    const int status = f(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // [rows, cols] or [G, M_max, cols]: a tensor of `kind`, or a pair (e4m3 codes, scales) as a GEMM's lhs.
 struct RowOperand {
     const at::Tensor *a = nullptr, *sf = nullptr;
@@ -164,14 +173,15 @@ int sort_contiguous(const Call &c) {
     const Sorted s = sort_args(c, 1, 3);
     const at::Tensor &m = c.dims(2, "m_indices", 1, 1);
     c.check(m, "m_indices", m.sizes(), I32);
-    return dg_moe_sort_contiguous(ptr(s.ids), id_bytes(s), s.T, s.k, s.G, size(m, 0), ptr<int>(s.rows), ptr<int>(m),
-                                  ptr<int>(s.counts), c.stream());
+    return without_lock(dg_moe_sort_contiguous, ptr(s.ids), id_bytes(s), s.T, s.k, s.G, size(m, 0), ptr<int>(s.rows),
+                        ptr<int>(m), ptr<int>(s.counts), c.stream());
 }
 
 // (topk_ids, row_of_slot, counts)
 int sort_nopad(const Call &c) {
     const Sorted s = sort_args(c, 1, 2);
-    return dg_moe_sort_nopad(ptr(s.ids), id_bytes(s), s.T, s.k, s.G, ptr<int>(s.rows), ptr<int>(s.counts), c.stream());
+    return without_lock(dg_moe_sort_nopad, ptr(s.ids), id_bytes(s), s.T, s.k, s.G, ptr<int>(s.rows), ptr<int>(s.counts),
+                        c.stream());
 }
 
 int integer(PyObject *o, const char *name) {
@@ -196,8 +206,8 @@ float number(PyObject *o, const char *name) {
 // (topk_ids, row_of_slot, masked_m, m_max)
 int sort_masked(const Call &c) {
     const Sorted s = sort_args(c, 1, 2);
-    return dg_moe_sort_masked(ptr(s.ids), id_bytes(s), s.T, s.k, s.G, integer(c.args[3], "m_max"), ptr<int>(s.rows),
-                              ptr<int>(s.counts), c.stream());
+    return without_lock(dg_moe_sort_masked, ptr(s.ids), id_bytes(s), s.T, s.k, s.G, integer(c.args[3], "m_max"),
+                        ptr<int>(s.rows), ptr<int>(s.counts), c.stream());
 }
 
 // (x, row_of_slot, out)
@@ -206,8 +216,8 @@ int permute(const Call &c) {
     c.check(x, "x", x.sizes(), ACT);
     c.check(row, "row_of_slot", {x.size(0), row.size(1)}, I32);
     const RowOperand out = row_operand(c, 2, "out", x.size(1), same_as(x));
-    return dg_moe_permute(ptr(x), code(x), ptr<int>(row), size(x, 0), size(row, 1), size(x, 1), out.rows, out.rows_per_group,
-                          ptr(out.a), ptr<float>(out.sf), c.stream());
+    return without_lock(dg_moe_permute, ptr(x), code(x), ptr<int>(row), size(x, 0), size(row, 1), size(x, 1), out.rows,
+                        out.rows_per_group, ptr(out.a), ptr<float>(out.sf), c.stream());
 }
 
 const at::Tensor &rows_in(const Call &c, int i, int &n) {
@@ -227,8 +237,8 @@ int unpermute(const Call &c) {
     c.check(row, "row_of_slot", row.sizes(), I32);
     c.check(out, "out", {row.size(0), rows.size(-1)}, same_as(rows));
     c.check(w, "weights", row.sizes(), F32);
-    return dg_moe_unpermute(ptr(rows), code(rows), ptr<int>(row), ptr<float>(w), size(row, 0), size(row, 1), size(rows, -1), n,
-                            ptr(out), c.stream());
+    return without_lock(dg_moe_unpermute, ptr(rows), code(rows), ptr<int>(row), ptr<float>(w), size(row, 0), size(row, 1),
+                        size(rows, -1), n, ptr(out), c.stream());
 }
 
 // (d_out, rows, row_of_slot, weights, d_rows, d_weights)
@@ -243,9 +253,9 @@ int unpermute_backward(const Call &c) {
     const RowOperand d = row_operand(c, 4, "d_rows", rows.size(-1), same_as(rows));
     if (d.a->sizes() != rows.sizes())
         refuse("d_rows must be shaped as rows, %s, got %s", text(rows.sizes()).c_str(), text(d.a->sizes()).c_str());
-    return dg_moe_unpermute_backward(ptr(d_out), ptr(rows), code(rows), ptr<int>(row), ptr<float>(w), size(row, 0),
-                                     size(row, 1), size(rows, -1), n, d.rows_per_group, ptr(d.a), ptr<float>(d.sf),
-                                     ptr<float>(d_w), c.stream());
+    return without_lock(dg_moe_unpermute_backward, ptr(d_out), ptr(rows), code(rows), ptr<int>(row), ptr<float>(w), size(row,
+                        0), size(row, 1), size(rows, -1), n, d.rows_per_group, ptr(d.a), ptr<float>(d.sf), ptr<float>(d_w),
+                        c.stream());
 }
 
 // (d_out or None, gate_up, out or d_gate_up, m_indices, counts, masked_m): None for d_out is the forward
@@ -278,10 +288,10 @@ int swiglu(const Call &c) {
     if (grouped != (masked != nullptr) || (masked && G != gu.size(0)))
         refuse("tensors of three dims [G, M_max, ...] go with masked_m [G], and masked_m with them");
     if (d_out)
-        return dg_swiglu_backward(ptr(d_out), ptr(gu), code(gu), out.rows, static_cast<int>(I), ptr<int>(m), ptr<int>(counts),
-                                  ptr<int>(masked), G, ptr(out.a), ptr<float>(out.sf), c.stream());
-    return dg_swiglu(ptr(gu), code(gu), out.rows, static_cast<int>(I), ptr<int>(m), ptr<int>(counts), ptr<int>(masked), G,
-                     ptr(out.a), ptr<float>(out.sf), c.stream());
+        return without_lock(dg_swiglu_backward, ptr(d_out), ptr(gu), code(gu), out.rows, static_cast<int>(I), ptr<int>(m),
+                            ptr<int>(counts), ptr<int>(masked), G, ptr(out.a), ptr<float>(out.sf), c.stream());
+    return without_lock(dg_swiglu, ptr(gu), code(gu), out.rows, static_cast<int>(I), ptr<int>(m), ptr<int>(counts),
+                        ptr<int>(masked), G, ptr(out.a), ptr<float>(out.sf), c.stream());
 }
 
 // (x, weight, out, eps, rstd)
@@ -299,8 +309,8 @@ int rms_norm(const Call &c) {
     }
     const RowOperand out = row_operand(c, 2, "out", x.size(1), kind);
     if (out.a->sizes() != x.sizes()) refuse("out must be %s, got %s", text(x.sizes()).c_str(), text(out.a->sizes()).c_str());
-    return dg_rms_norm(ptr(x), code(x), ptr(w), code(w), number(c.args[3], "eps"), size(x, 0), size(x, 1), ptr(out.a),
-                       kind == F32 ? DG_F32 : DG_BF16, ptr<float>(out.sf), ptr<float>(rstd), c.stream());
+    return without_lock(dg_rms_norm, ptr(x), code(x), ptr(w), code(w), number(c.args[3], "eps"), size(x, 0), size(x, 1),
+                        ptr(out.a), kind == F32 ? DG_F32 : DG_BF16, ptr<float>(out.sf), ptr<float>(rstd), c.stream());
 }
 
 // (d_out, x, weight, rstd, d_x, d_weight, d_skip)
@@ -315,8 +325,8 @@ int rms_norm_backward(const Call &c) {
     c.check(d_x, "d_x", x.sizes(), same_as(x));
     c.check(d_w, "d_weight", {x.size(1)}, F32);
     c.check(skip, "d_skip", x.sizes(), same_as(x));
-    return dg_rms_norm_backward(ptr(d_out), ptr(skip), ptr(x), code(x), code(d_out), ptr(w), code(w), ptr<float>(rstd),
-                                size(x, 0), size(x, 1), ptr(d_x), ptr<float>(d_w), c.stream());
+    return without_lock(dg_rms_norm_backward, ptr(d_out), ptr(skip), ptr(x), code(x), code(d_out), ptr(w), code(w),
+                        ptr<float>(rstd), size(x, 0), size(x, 1), ptr(d_x), ptr<float>(d_w), c.stream());
 }
 
 // weight, weight_post and a gate [H] have one type, bf16 or fp32; a gate [T, H] has y's.
@@ -361,9 +371,9 @@ int residual_rms_norm(const Call &c) {
         if (out.a->sizes() != x.sizes())
             refuse("out must be %s, got %s", text(x.sizes()).c_str(), text(out.a->sizes()).c_str());
     }
-    return dg_residual_rms_norm(ptr(x), code(x), ptr(y), code(y), ptr(p.w), ptr(p.w_post), ptr(p.gate), p.gate_kind, p.type,
-                                number(c.args[7], "alpha"), number(c.args[8], "eps"), size(x, 0), size(x, 1), ptr(x_out),
-                                ptr(out.a), ptr<float>(out.sf), ptr<float>(rstd), ptr<float>(rstd_post), c.stream());
+    return without_lock(dg_residual_rms_norm, ptr(x), code(x), ptr(y), code(y), ptr(p.w), ptr(p.w_post), ptr(p.gate),
+                        p.gate_kind, p.type, number(c.args[7], "alpha"), number(c.args[8], "eps"), size(x, 0), size(x, 1),
+                        ptr(x_out), ptr(out.a), ptr<float>(out.sf), ptr<float>(rstd), ptr<float>(rstd_post), c.stream());
 }
 
 // (d_x_out, y, d_x, d_y, d_out, x_out, weight, rstd, weight_post, rstd_post, gate, alpha, d_weight, d_weight_post, d_gate)
@@ -386,10 +396,10 @@ int residual_rms_norm_backward(const Call &c) {
     c.check(d_w_post, "d_weight_post", {H}, F32);
     if (p.gate_kind == 1) c.check(d_gate, "d_gate", {H}, F32);
     else c.check(d_gate, "d_gate", y.sizes(), same_as(y));
-    return dg_residual_rms_norm_backward(ptr(d_x_out), ptr(d_out), ptr(x_out), code(d_x), ptr(y), code(y), ptr(p.w),
-                                         ptr(p.w_post), ptr(p.gate), p.gate_kind, p.type, number(c.args[11], "alpha"),
-                                         ptr<float>(rstd), ptr<float>(rstd_post), size(y, 0), size(y, 1), ptr(d_x), ptr(d_y),
-                                         ptr<float>(d_w), ptr<float>(d_w_post), ptr(d_gate), c.stream());
+    return without_lock(dg_residual_rms_norm_backward, ptr(d_x_out), ptr(d_out), ptr(x_out), code(d_x), ptr(y), code(y),
+                        ptr(p.w), ptr(p.w_post), ptr(p.gate), p.gate_kind, p.type, number(c.args[11], "alpha"),
+                        ptr<float>(rstd), ptr<float>(rstd_post), size(y, 0), size(y, 1), ptr(d_x), ptr(d_y), ptr<float>(d_w),
+                        ptr<float>(d_w_post), ptr(d_gate), c.stream());
 }
 
 PyObject *raise(int status, const char *message) {

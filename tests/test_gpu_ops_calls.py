@@ -4,6 +4,7 @@ import os
 import subprocess
 import sys
 import threading
+import time
 
 import numpy as np
 import pytest
@@ -217,3 +218,36 @@ def test_sort_takes_no_more_sms_than_the_cap(T, k, G, kind):
     assert done.returncode == 0, done.stderr[-2000:]
     plans = [int(line.rsplit("ctas=", 1)[1]) for line in done.stderr.splitlines() if line.startswith("[dg] sort")]
     assert plans == [n for n in (16, *clusters.values()) for _ in range(2)]  # (both layouts)
+
+
+def test_a_launch_that_waits_leaves_the_interpreter_to_other_threads(dg):
+    """Behind a kernel of half a second the queue of launches fills up and a call waits in it; other Python threads go on."""
+    x, w, out = torch.randn(8, 128, device="cuda"), torch.ones(128, device="cuda"), torch.empty(8, 128, device="cuda")
+    dg.rms_norm(x, w, out)
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    done, gaps, waits = threading.Event(), [0.0], [0.0]
+
+    def tick():
+        last = time.perf_counter()
+        while not done.is_set():
+            time.sleep(1e-3)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    thread = threading.Thread(target=tick)
+    thread.start()
+    try:
+        torch.cuda._sleep(1_000_000_000)  # (cycles)
+        begin = time.perf_counter()
+        while time.perf_counter() - begin < 0.2 and max(waits) < 0.1 and len(waits) < 50_000:
+            t = time.perf_counter()
+            dg.rms_norm(x, w, out)
+            waits.append(time.perf_counter() - t)
+    finally:
+        done.set()
+        thread.join()
+        torch.cuda.synchronize()
+    assert max(waits) > 0.1, "no launch had to wait: this shows nothing"
+    assert max(gaps) < max(waits) / 2, (max(gaps), max(waits))
