@@ -253,9 +253,9 @@ int unpermute_backward(const Call &c) {
     const RowOperand d = row_operand(c, 4, "d_rows", rows.size(-1), same_as(rows));
     if (d.a->sizes() != rows.sizes())
         refuse("d_rows must be shaped as rows, %s, got %s", text(rows.sizes()).c_str(), text(d.a->sizes()).c_str());
-    return without_lock(dg_moe_unpermute_backward, ptr(d_out), ptr(rows), code(rows), ptr<int>(row), ptr<float>(w), size(row,
-                        0), size(row, 1), size(rows, -1), n, d.rows_per_group, ptr(d.a), ptr<float>(d.sf), ptr<float>(d_w),
-                        c.stream());
+    return without_lock(dg_moe_unpermute_backward, ptr(d_out), ptr(rows), code(rows), ptr<int>(row), ptr<float>(w),
+                        size(row, 0), size(row, 1), size(rows, -1), n, d.rows_per_group, ptr(d.a), ptr<float>(d.sf),
+                        ptr<float>(d_w), c.stream());
 }
 
 // (d_out or None, gate_up, out or d_gate_up, m_indices, counts, masked_m): None for d_out is the forward

@@ -111,26 +111,26 @@ __global__ void __launch_bounds__(32 * SWIGLU_WARPS, BACKWARD ? 3 : 4) swiglu_ke
                     for (int i = 0; i < VEC; ++i) b[i] = 1.f - a[i];
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) b[i] = fmaf(g[i], b[i], 1.f);
-                    mul_vec(u, b);  // u (1 + g (1 - s))
+                    // s is 0 where g is far below zero, so it comes first: u (1 + g (1 - s)) may pass the largest number
                     mul_vec(a, d);  // d s
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) b[i] = a[i];
-                    mul_vec(b, g);
-                    mul_vec(a, u);
+                    mul_vec(b, a);
+                    mul_vec(b, u);  // d_g
+                    mul_vec(a, g);  // d_u
                 }
+                auto &left = BACKWARD ? b : a, &right = a;  // the output's columns from 0 and (gradient) from I on
                 const long long at = static_cast<long long>(row0 + first + r) * (BACKWARD ? 2 : 1) * p.I + col;
                 if constexpr (FP8) {
                     float scale;
                     uint8_t *out = static_cast<uint8_t *>(p.out) + at;
-                    *reinterpret_cast<uint2 *>(out) = quantise(a, block_amax(a, col, p.I), scale);
+                    *reinterpret_cast<uint2 *>(out) = quantise(left, block_amax(left, col, p.I), scale);
                     if ((lane & (BLOCK_LANES - 1)) == r) keep = scale;
                     if constexpr (BACKWARD) {
-                        *reinterpret_cast<uint2 *>(out + p.I) = quantise(b, block_amax(b, col, p.I), scale);
+                        *reinterpret_cast<uint2 *>(out + p.I) = quantise(right, block_amax(right, col, p.I), scale);
                         if ((lane & (BLOCK_LANES - 1)) == r) keep_u = scale;
                     }
                 } else {
-                    store_vec(static_cast<T *>(p.out) + at, a);
-                    if constexpr (BACKWARD) store_vec(static_cast<T *>(p.out) + at + p.I, b);
+                    store_vec(static_cast<T *>(p.out) + at, left);
+                    if constexpr (BACKWARD) store_vec(static_cast<T *>(p.out) + at + p.I, right);
                 }
             }
         if constexpr (FP8) {
