@@ -131,10 +131,10 @@ __device__ __forceinline__ void fma_vec(float (&c)[VEC], const float (&a)[VEC], 
 #pragma unroll
     for (int i = 0; i < VEC; i += 2) fma2(c[i], c[i + 1], a[i], a[i + 1], s, s);
 }
-__device__ __forceinline__ void add_vec(float (&a)[VEC], float s) {
+__device__ __forceinline__ void one_plus_times(float (&a)[VEC], float s) {  // a = (1 + a) * s for a power of two s
 #pragma unroll
     for (int i = 0; i < VEC; i += 2)
-        asm("{.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tadd.rn.f32x2 a, a, b;\n\t"
+        asm("{.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tfma.rn.f32x2 a, a, b, b;\n\t"
             "mov.b64 {%0, %1}, a;}"
             : "+f"(a[i]), "+f"(a[i + 1])
             : "f"(s));

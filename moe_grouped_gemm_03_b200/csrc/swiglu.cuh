@@ -28,9 +28,11 @@ struct SwigluParams {
     int across;           // warps side by side in a row: 1, 2, 4 or 8
 };
 
-// s = sigmoid(g).  FAST, for bf16 and e4m3 results: exp and the reciprocal by their approximating instructions, each within a
-// few 2^-23 (|g| < 20), far below half a step of the result, 2^-8 or 2^-4 (fp32 to e4m3, 16976 x 4608: 86 us, 107 without).
-// exp(-g) of a large negative g is infinite and its reciprocal 0, as it should be.
+// s = sigmoid(g).  FAST, for bf16 and e4m3 results: exp and the reciprocal by their approximating instructions, off by (2 + |g|)
+// 2^-23 of s, far below half a step of the result, 2^-8 or 2^-4 (fp32 to e4m3, 16976 x 4608: 86 us, 107 without).  The reciprocal
+// is that of a quarter of 1 + exp(-g): the instruction has no results below 2^-126, which s falls to at g = -87.3 (the factor makes
+// bf16 results 0.5% slower and e4m3 ones 0.5 to 2%, 69632 x 2048 124.6 us in place of 122.2).  From g = -88.7 down exp(-g) is
+// infinite, in both forms, and s is 0.
 template <bool FAST> __device__ __forceinline__ void sigmoid(const float (&g)[VEC], float (&s)[VEC]) {
     if constexpr (FAST) {
 #pragma unroll
@@ -38,9 +40,10 @@ template <bool FAST> __device__ __forceinline__ void sigmoid(const float (&g)[VE
         mul_vec(s, -1.4426950408889634f);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
-        add_vec(s, 1.f);
+        one_plus_times(s, 0.25f);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+        mul_vec(s, 0.25f);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) s[i] = 1.f / (1.f + expf(-g[i]));

@@ -59,3 +59,31 @@ def test_swiglu_gradient_of_large_finite_values_to_e4m3(dg):
     want[0, 0] = 1.5  # d u / 2
     q, s = ref.quantise(want)
     assert (got == q).all() and (sf[:, 0].cpu().double().numpy() == s[0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_swiglu_of_gates_whose_sigmoid_is_not_a_normal_number(dg, dtype, fp8):
+    """Between -88.7 and -87.3 sigmoid is below 2^-126 but not 0: g s u is a normal number for a u large enough."""
+    g = torch.linspace(-88.625, -86.0, 128).to(dtype)
+    assert float(g.min()) > -88.72  # (exp(-g) is finite in 32 bits down to there)
+    gu = torch.cat([g, torch.full((128,), 2.0 ** 100, dtype=dtype)])[None].cuda()
+    d = torch.ones(1, 128, dtype=dtype, device="cuda")
+    forward, gradient = ref.swiglu(gu).numpy(), ref.swiglu_backward(d, gu).numpy()
+    # exp's argument is rounded twice (89 2^-24 each), s below the normal numbers to 2^-150 of at least 2^-128: below 2^-16
+    err = 2.0 ** -16
+    for want, call, cols in ((forward, lambda o: dg.swiglu(gu, o), 128), (gradient, lambda o: dg.swiglu_backward(d, gu, o), 256)):
+        if not fp8:
+            out = torch.full((1, cols), -7.5, dtype=dtype, device="cuda")
+            call(out)
+            equal_but_for(out, want, np.abs(want) * (HALF[dtype] + err))
+            continue
+        codes, sf = torch.zeros(1, cols, dtype=torch.uint8, device="cuda"), torch.zeros(cols // 128, 4, device="cuda")
+        call((codes, sf))
+        s = sf[:, 0].cpu().double().numpy()
+        top = np.abs(want).reshape(-1, 128).max(1)
+        assert ((s >= ref.scale_of(top * (1 - err))) & (s <= ref.scale_of(top * (1 + err)))).all()
+        wide = np.repeat(s, 128)[None]
+        got = codes.view(torch.float8_e4m3fn).double().cpu().numpy() * wide
+        equal_but_for(got, want, np.maximum(np.abs(want) * (1 + err) * 2.0 ** -4, wide * 2.0 ** -10) + np.abs(want) * err)
+    dg.check_device_error()
