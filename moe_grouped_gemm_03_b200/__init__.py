@@ -41,11 +41,25 @@ if not os.path.exists(LIB_PATH):
                       "(or __graft_entry__.build()); there is no non-CUDA implementation")
 
 _lib = ctypes.CDLL(LIB_PATH)
-if not os.path.exists(os.path.join(_HERE, "_rowwise.so")):
-    raise ImportError(f"{os.path.join(_HERE, '_rowwise.so')} is missing: build it with __graft_entry__.build()")
-from . import _rowwise  # noqa: E402  (the binding of the row-wise operators, linked to libdg.so)
 
-_rowwise.set_error(DGError)
+
+class _NoBinding:
+    """In the place of _rowwise where it cannot be loaded: the GEMMs do without it, every call of the others raises."""
+
+    def __init__(self, error):
+        self._error = error
+
+    def __getattr__(self, name):
+        raise ImportError(f"{os.path.join(_HERE, '_rowwise.so')} cannot be loaded ({self._error}): build it against the "
+                          "installed torch with __graft_entry__.build()")
+
+
+try:
+    from . import _rowwise  # noqa: E402  (the binding of the row-wise operators, linked to libdg.so)
+except ImportError as _e:
+    _rowwise = _NoBinding(str(_e))
+else:
+    _rowwise.set_error(DGError)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _LL = ctypes.c_longlong
@@ -438,7 +452,7 @@ def m_grouped_fp8_gemm_nt_nopad(lhs, rhs, out: torch.Tensor, counts: torch.Tenso
 
 # --------------------------------------------------------------------------- dispatch, combine, SwiGLU and norms
 # Checked and called in _rowwise (csrc/rowwise_binding.cpp): contiguous CUDA tensors on the current device, on whose current
-# stream the calls run; DGError for anything else.
+# stream the calls run; DGError for anything else, ImportError if _rowwise.so is missing or of another torch.
 def get_m_total_bound(num_slots: int, num_groups: int) -> int:
     """Rows the contiguous layout needs at most for num_slots routed slots and num_groups groups (the size of m_indices,
     and of the GEMM's operands, when the counts are known on the device only)."""

@@ -66,7 +66,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
     if force or not _newer(BINDING, BINDING_DEPS):
-        build_binding()
+        try:
+            import torch  # noqa: F401
+        except ImportError:  # the C library needs none of it
+            print(f"no torch: {BINDING}, the Python binding of the row-wise operators, is not built", file=sys.stderr)
+        else:
+            build_binding()
     return LIB
 
 
