@@ -90,7 +90,11 @@ DG_EXPORT int dg_set_m_alignment_for_contiguous_layout(int alignment);
 DG_EXPORT int dg_get_tma_aligned_size(int mn, int elem_bytes);
 
 /* Cap on the persistent grid (README "Utilities": set_num_sms / get_num_sms).  n <= 0 restores the
- * default (every SM of the current device).  Returns the value now in force, or a negative status. */
+ * default (every SM of the current device).  Returns the value now in force, or a negative status.
+ *   GEMMs: at most n CTAs, one an SM.  dg_moe_sort_*: a cluster of at most n CTAs.  Gradients of the norms: n times the
+ *   CTAs that fit an SM, which the GPU may spread over more than n SMs; the sums for the parameters' gradients, and so
+ *   their last bits, go by that number.  dg_moe_permute, dg_moe_unpermute and its gradient, dg_swiglu and its gradient
+ *   and the forward norms launch a grid by their rows and take any SM: the cap does not hold for them. */
 DG_EXPORT int dg_set_num_sms(int n);
 DG_EXPORT int dg_get_num_sms(void);
 
@@ -233,11 +237,15 @@ DG_EXPORT int dg_fp8_gemm_nt_noalloc(const void *a, const float *sfa, const void
  *     2^ceil(log2(amax / 448)) (1 for a block of zeros, at least 2^-126), the codes are round-to-nearest-even of
  *     value / scale.  An infinite or NaN value becomes e4m3's NaN code, and its block's scale goes by the others.
  *   - Sums, means and products are fp32 and rounded once.  Nothing depends on the order in which CTAs run: the same
- *     inputs give the same bits.
+ *     inputs give the same bits (under one setting of dg_set_num_sms).
  *   - Rows that no slot or group owns are left as they were.
  *   - Outputs must not overlap inputs or each other, except where a call says so.
  *   - Each call is asynchronous on `stream` and takes no memory, but for the gradients of the norms (stream-ordered
- *     scratch for the parameters' sums).  An empty call (no tokens or rows) launches nothing.
+ *     scratch for the parameters' sums).  An empty call (no tokens or rows) writes no rows and, but for what sums over no
+ *     rows (the sort's counts and m_indices, the parameters' gradients), launches nothing.
+ *   - They make the operands of the forward GEMMs and of the data gradients (the NN call reads the forward weights).  The
+ *     operands of the weight gradients, e4m3 along the tokens as dg_k_grouped_fp8_gemm_nt_contiguous takes them, are not
+ *     among their outputs.
  */
 typedef enum { DG_BF16 = 0, DG_F32 = 1 } dg_dtype;
 
@@ -284,7 +292,11 @@ DG_EXPORT int dg_moe_unpermute_backward(const void *d_out, const void *rows_in, 
 /* SwiGLU on the rows that the groups own: out = g * sigmoid(g) * u with gate_up [R][2 I] = [g | u].  Rows: one of
  * m_indices [R] (contiguous), counts [G] (no padding) and masked_m [G] (masked, R = G * M_max), as the GEMM that wrote
  * gate_up took it; all NULL: every row.  G is read with counts and masked_m.  out [R][I] of `type`, or e4m3 with out_sf.
- * The gradient writes d_gate_up [R][2 I] = [d_g | d_u] from d_out [R][I]. */
+ * The gradient writes d_gate_up [R][2 I] = [d_g | d_u] from d_out [R][I].
+ * Counts out of range are clipped to the rows there are (negative ones to 0; the sum of counts to R, masked_m to M_max) and
+ * a row with any m_indices >= 0 is owned: nothing is recorded here, the GEMM before has recorded it.
+ * sigmoid counts as 0 where exp(-g) is infinite in fp32 (g < -88.7); with bf16 and e4m3 results exp and the reciprocal are
+ * approximations, off by (2 + |g|) 2^-23. */
 DG_EXPORT int dg_swiglu(const void *gate_up, int type, int R, int I, const int *m_indices, const int *counts,
                         const int *masked_m, int G, void *out, float *out_sf, dg_stream_t stream);
 DG_EXPORT int dg_swiglu_backward(const void *d_out, const void *gate_up, int type, int R, int I, const int *m_indices,

@@ -220,6 +220,45 @@ def test_sort_takes_no_more_sms_than_the_cap(T, k, G, kind):
     assert plans == [n for n in (16, *clusters.values()) for _ in range(2)]  # (both layouts)
 
 
+@pytest.mark.parametrize("cap", [1, 5])
+def test_norm_gradients_under_a_cap(dg, cap):
+    """Rows do not depend on set_num_sms; the parameters' gradients do by the order of their sums, over 600 rows."""
+    call = NormGradient(dg, 600, 1024, 6)
+    want = alone([call])[0]
+    dg.set_num_sms(cap)
+    try:
+        call(torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+    finally:
+        dg.set_num_sms(0)
+    d_x, d_y, d_w, d_wp, d_gate = call.outputs()
+    assert torch.equal(d_x, want[0]) and torch.equal(d_y, want[1])
+    i = call.inputs
+    x, y, w, wp, gate, dxo, do = (i[n].double() for n in ("x_out", "y", "weight", "weight_post", "gate", "d_x_out", "d_out"))
+    got = ref.norm_backward(*(i[n] for n in ("d_x_out", "d_out", "x_out", "y", "weight", "weight_post", "gate")), 1.0, i["rstd"],
+                            i["rstd_post"])
+    e = (w * do).abs()
+    sx = dxo.abs() + e + x.abs() * (e * x.abs()).mean(1, keepdim=True)  # size of the terms of d_x (r = 1)
+    # chains of at most 600 additions for a parameter and 2^6 for a row: below 2^10 roundings of the terms' sizes
+    for out, name, size in ((d_w, "d_w", do.abs() * x.abs()), (d_wp, "d_w_post", gate.abs() * sx * y.abs()),
+                            (d_gate, "d_gate", wp.abs() * sx * y.abs())):
+        assert bool(((out.double().cpu() - got[name]).abs() <= size.sum(0).cpu() * 2.0 ** -14).all()), name
+    dg.check_device_error()
+
+
+def test_swiglu_clips_counts_and_records_nothing(dg):
+    """As documented: counts out of range are clipped to the rows there are, and the error word stays clear."""
+    gu = torch.randn(12, 256, device="cuda").to(BF16)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for shape, kw, owned in (((12, 256), dict(counts=i32(-3, 5, 100)), range(12)), ((12, 256), dict(counts=i32(-3, 5)), range(5)),
+                             ((3, 4, 256), dict(masked_m=i32(-1, 9, 2)), [4, 5, 6, 7, 8, 9]),
+                             ((12, 256), dict(m_indices=i32(*[-1, 2, 1 << 30] * 4)), [t for t in range(12) if t % 3])):
+        out = torch.full((*shape[:-1], 128), -7.5, dtype=BF16, device="cuda")
+        dg.swiglu(gu.view(shape), out, **kw)
+        dg.check_device_error()
+        assert sorted(set((out.view(12, 128) != -7.5).any(1).nonzero()[:, 0].tolist())) == list(owned)
+
+
 def test_a_launch_that_waits_leaves_the_interpreter_to_other_threads(dg):
     """Behind a kernel of half a second the queue of launches fills up and a call waits in it; other Python threads go on."""
     x, w, out = torch.randn(8, 128, device="cuda"), torch.ones(128, device="cuda"), torch.empty(8, 128, device="cuda")
