@@ -333,9 +333,10 @@ template <auto Kernel> int launch_norm_ring(const dg::NormParams &p, const NormS
 
 template <typename X, typename Y, bool FP8> int launch_norm(const dg::NormParams &p, int sms, dg_stream_t stream) {
     // 8 elements a thread while all rows' vectors fit on the SMs together (the call is then one row long); with many rows 32, so
-    // that fewer warps take part in the sums (bf16, 8192 x 8192: 92 us, 113 with 16), but 16 up to 16 times what fits (4000 x
-    // 4096: 32 us, 33 with 32; 1344 x 5888: 22, 23) and with fp32 outputs, whose rows wait longer for memory (8192 x 8192: 139
-    // us, 151 with 32; 1344 x 5888: 27, 32)
+    // that fewer warps take part in the sums, but 16 up to 16 times what fits, and with fp32 outputs, whose rows wait longer for
+    // memory.  Residual norm with w_post and a gate [H] (rms_norm alone), us with 16 and with 32: bf16 8192 x 8192 109 and 95
+    // (64, 48), 4000 x 4096 29 and 29 (16.5, 13.5), 1344 x 5888 17 and 20 (6.7, 6.5), 16000 x 1024 27 and 29 (18, 18); all
+    // fp32 8192 x 8192 163 and 169, 1344 x 5888 25 and 31.
     const int vecs = p.H / dg::VEC;
     const long long vecs_per_sm = (p.T * static_cast<long long>(vecs) + sms - 1) / sms;
     const int iters = vecs > dg::NORM_MAX_THREADS                   ? 4
@@ -347,7 +348,8 @@ template <typename X, typename Y, bool FP8> int launch_norm(const dg::NormParams
         return launch("norm launch", kernel, dim3(static_cast<unsigned>(p.T)), dim3(((vecs + iters - 1) / iters + 31) / 32 * 32),
                       0, 1, stream, p);
     }
-    // a row a warp: 16384 rows of 256 in 8 us (18 with a row a CTA), of 512 in 16 (21), of 1024 in 28 (29) but 36 (33) in e4m3
+    // a row a warp: 16384 rows in bf16, rms_norm of 256 columns 3.9 us (17.5 with a row a CTA), of 512 6.0 (17.7); residual norm
+    // with w_post and a gate [H] 6.1 (17.6) and 15.6 (20.3).  1024 columns gained 3% in bf16 and lost 9% to e4m3.
     auto kernel = vecs <= 32 ? dg::rms_norm_kernel<X, Y, FP8, 1, true> : dg::rms_norm_kernel<X, Y, FP8, 2, true>;
     return launch("norm launch", kernel, dim3((p.T + dg::NORM_ROW_WARPS - 1) / dg::NORM_ROW_WARPS),
                   dim3(32 * dg::NORM_ROW_WARPS), 0, 1, stream, p);

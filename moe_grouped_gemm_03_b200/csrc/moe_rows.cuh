@@ -6,7 +6,8 @@
 //   unpermute          out[t] = sum_s w(t, s) * rows[row(t, s)]
 //   its gradient       d_rows[row(t, s)] = w(t, s) * d_out[t],  d_w(t, s) = <d_out[t], rows[row(t, s)]>
 //
-// All are bound by HBM: every byte of a token's row is read once, whatever k is.
+// All are bound by HBM.  Permute reads a token's row once, whatever k is, and unpermute each expert row once; the gradient
+// reads d_out's row, and finds its blocks' largest values, once for every 8 slots of the token (the second time from L2).
 #pragma once
 #include "rowwise.cuh"
 

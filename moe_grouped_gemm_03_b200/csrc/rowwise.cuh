@@ -27,8 +27,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// (stream: a load of what is read once and need not stay in L1.)
-
 // Asynchronous copies of 16 bytes to shared memory, past L1, waited for in groups by the thread that made them.
 __device__ __forceinline__ void copy_async16(void *s, const void *p) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s)), "l"(p) : "memory");
