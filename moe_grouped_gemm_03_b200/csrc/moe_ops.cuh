@@ -83,7 +83,10 @@ template <typename Id, bool ONE> int prepare_sort(int device, int &most) {
     constexpr auto kernel = dg::moe_sort_kernel<Id, ONE>;
     constexpr int kMostShared = static_cast<int>(sizeof(int)) * dg::sort_smem_words(dg::SORT_MAX_WARPS, dg::SORT_MAX_GROUPS);
     if (int rc = allow_shared<kernel>(device, kMostShared, "cudaFuncSetAttribute (sort)")) return rc;
-    if (most > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) most = 8;
+    if (most > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();  // (what the runtime refuses here is no error of the call)
+        most = 8;
+    }
     for (; most > 1; most = most > 8 ? 8 : 1) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(most);
@@ -96,9 +99,9 @@ template <typename Id, bool ONE> int prepare_sort(int device, int &most) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0) break;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) cudaGetLastError();
+        else if (clusters > 0) break;
     }
-    cudaGetLastError();  // (what the runtime refused here is no error of the call)
     return DG_OK;
 }
 
